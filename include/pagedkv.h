@@ -70,6 +70,7 @@ typedef enum { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
 #define PA_DEV_BAD_SLOT 0x2
 #define PA_DEV_BAD_PAIR 0x4
 #define PA_DEV_BAD_CONTEXT_LEN 0x8
+#define PA_DEV_BAD_KEEP 0x20 /* a kept position or count out of range (pa_compact_tokens) */
 #define PA_DEV_TIMEOUT 0x10 /* a pipeline wait gave up after ~2 s; outputs are invalid */
 
 /* Library ABI version (major*100 + minor). */
@@ -144,6 +145,45 @@ pa_status pa_decode_multi(void* out, const void* q, const void* k_cache, const v
                           int block_size, int max_blocks_per_seq, int num_blocks, float scale,
                           pa_dtype dtype, void* workspace, size_t workspace_bytes,
                           int32_t* dev_status, void* stream);
+
+/*
+ * pa_decode_window -- pa_decode_multi with a sliding window and a few first tokens that stay
+ * visible.
+ *
+ * Defined by the passages of pa_decode and pa_decode_multi, the visible positions restricted:
+ * new token j of sequence s, at position p = context_lens[s] - q_len + j, sees
+ *   { t : 0 <= t <= p and (t > p - window or t < num_sinks) }
+ * and out[s][j][h][:] is the softmax over those positions only.  window >= 1 counts the
+ * token itself; num_sinks >= 0; window >= context_lens[s] is pa_decode_multi's mask.
+ *
+ * A position that no new token of its sequence sees is never used, and a block-table entry
+ * whose whole block is such positions is never read: it may hold anything (the pages behind
+ * the window can be given back, pa_bm_drop_window), as may the cache slots themselves (NaN
+ * included).  The rows that some new token sees must be finite for all of its sequence's.
+ * Only the visible rows are read from the caches, so the time goes with the window, not the
+ * context.
+ *
+ *   q, out         [num_seqs][q_len][num_q_heads][head_dim]
+ *   other arguments, limits, workspace and errors as for pa_decode_multi; PA_ERR_INVALID for
+ *   window < 1 or num_sinks < 0.
+ *
+ * pa_decode_window_e4m3_bs -- the same over 8-bit pools with per-(block, kv head) scales
+ * (format and limits of pa_decode_e4m3_bs: at most 16 query rows per kv head).
+ */
+pa_status pa_decode_window(void* out, const void* q, const void* k_cache, const void* v_cache,
+                           const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                           int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                           int block_size, int max_blocks_per_seq, int num_blocks, int window,
+                           int num_sinks, float scale, pa_dtype dtype, void* workspace,
+                           size_t workspace_bytes, int32_t* dev_status, void* stream);
+pa_status pa_decode_window_e4m3_bs(void* out, const void* q, const void* k_cache,
+                                   const void* v_cache, const float* k_scales,
+                                   const float* v_scales, const int32_t* block_tables,
+                                   const int32_t* context_lens, int num_seqs, int q_len,
+                                   int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                   int max_blocks_per_seq, int num_blocks, int window,
+                                   int num_sinks, float scale, pa_dtype dtype, void* workspace,
+                                   size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /*
  * pa_decode_append -- pa_cache_append of each sequence's newest token fused into
@@ -370,6 +410,58 @@ pa_status pa_cache_append(void* k_cache, void* v_cache, const void* k, const voi
 pa_status pa_copy_blocks(void* const* k_caches, void* const* v_caches, int num_layers,
                          const int32_t* pairs, int num_pairs, int num_blocks,
                          size_t block_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * pa_compact_tokens -- the kept tokens of each sequence moved to the front of its pages: what
+ * a cache that evicts tokens runs to get the pages of the evicted ones back.
+ *
+ * Defined by [P1] "Why KV cache memory was the bottleneck" and [P2] "Core Principle" (blocks
+ * go back to the pool; a logical block is found through the sequence's table), with the
+ * kept positions chosen by the caller.  For every layer l, sequence s, kv head h and
+ * i < keep_lens[s], with t = keep[l][s][h][i] and bs the block size, in the K and the V pool:
+ *   cache[dst_tables[s][i / bs]][h][i % bs][:] = cache[src_tables[s][t / bs]][h][t % bs][:]
+ * (the right side as it was before the call), byte for byte.
+ *
+ *   k_caches, v_caches  HOST arrays of num_layers device pointers (one pool per layer)
+ *   src_tables     device int32 [num_seqs][src_blocks_per_seq], the tables before
+ *   dst_tables     device int32 [num_seqs][dst_blocks_per_seq], the tables after; entry i may
+ *                  be the sequence's own source entry i (in place) or a block that no source
+ *                  table of the call names (pa_bm_compact plans them)
+ *   context_lens   device int32 [num_seqs], the lengths before
+ *   keep           device int32 [num_layers or 1][num_seqs][num_kv_heads or 1][max_keep]:
+ *                  positions in [0, context_lens[s]), strictly ascending; the first dimension
+ *                  is num_layers when keep_per_layer is not 0, the third num_kv_heads when
+ *                  keep_per_head is not 0, else one selection serves all of them
+ *   keep_lens      device int32 [num_seqs], at most max_keep and the destination's room
+ *   elem_bytes     2 (16-bit pools) or 1 (8-bit pools with one scale per pool)
+ * Errors: PA_DEV_BAD_KEEP for a position or a count out of range (the row is skipped, the
+ * count clamped), PA_DEV_BAD_BLOCK_ID, PA_DEV_BAD_CONTEXT_LEN.  Positions that do not ascend,
+ * or tables that name a block twice, give undefined rows.  Cache rows past keep_lens[s] keep
+ * what they held.  No workspace.
+ *
+ * pa_compact_tokens_e4m3_bs -- the same over 8-bit pools with per-(block, kv head) scales
+ * (pa_cache_append_e4m3_bs): k_scales, v_scales are HOST arrays of num_layers device pointers
+ * to float [num_blocks][num_kv_heads].  A new block's scale is the one that the row at its
+ * offset 0 fixes (the append's rule, from that row's values scale * code), and each value of
+ * its rows becomes the E4M3 code of value / scale (nearest even, clamped to 448).
+ */
+pa_status pa_compact_tokens(void* const* k_caches, void* const* v_caches, int num_layers,
+                            const int32_t* src_tables, int src_blocks_per_seq,
+                            const int32_t* dst_tables, int dst_blocks_per_seq,
+                            const int32_t* context_lens, const int32_t* keep,
+                            const int32_t* keep_lens, int max_keep, int keep_per_layer,
+                            int keep_per_head, int num_seqs, int num_kv_heads, int head_dim,
+                            int elem_bytes, int block_size, int num_blocks, int32_t* dev_status,
+                            void* stream);
+pa_status pa_compact_tokens_e4m3_bs(void* const* k_caches, void* const* v_caches,
+                                    float* const* k_scales, float* const* v_scales,
+                                    int num_layers, const int32_t* src_tables,
+                                    int src_blocks_per_seq, const int32_t* dst_tables,
+                                    int dst_blocks_per_seq, const int32_t* context_lens,
+                                    const int32_t* keep, const int32_t* keep_lens, int max_keep,
+                                    int keep_per_layer, int keep_per_head, int num_seqs,
+                                    int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                    int32_t* dev_status, void* stream);
 
 /*
  * pa_swap_out_blocks / pa_swap_in_blocks -- the data side of preemption (see

@@ -13,6 +13,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "compact.cuh"
 #include "decode.cuh"
 #include "kv_ops.cuh"
 #include "launch.cuh"
@@ -151,6 +152,10 @@ pa_status dispatch_mode(bool kv8, bool wide, int mode, bool bf16, int d, int bs,
       return nc == 16 ? run_wide_mode<pkv::kAppend, 16>(bf16, d, bs, a, mk, mv, grid, s)
              : nc == 32 ? run_wide_mode<pkv::kAppend, 32>(bf16, d, bs, a, mk, mv, grid, s)
                         : run_wide_mode<pkv::kAppend, 64>(bf16, d, bs, a, mk, mv, grid, s);
+    if (mode == pkv::kWindow)
+      return nc == 16 ? run_wide_mode<pkv::kWindow, 16>(bf16, d, bs, a, mk, mv, grid, s)
+             : nc == 32 ? run_wide_mode<pkv::kWindow, 32>(bf16, d, bs, a, mk, mv, grid, s)
+                        : run_wide_mode<pkv::kWindow, 64>(bf16, d, bs, a, mk, mv, grid, s);
     return nc == 16 ? run_wide_mode<pkv::kPlain, 16>(bf16, d, bs, a, mk, mv, grid, s)
            : nc == 32 ? run_wide_mode<pkv::kPlain, 32>(bf16, d, bs, a, mk, mv, grid, s)
                       : run_wide_mode<pkv::kPlain, 64>(bf16, d, bs, a, mk, mv, grid, s);
@@ -161,6 +166,7 @@ pa_status dispatch_mode(bool kv8, bool wide, int mode, bool bf16, int d, int bs,
       case pkv::kPrefix: return run_decode_mode<pkv::kPrefix, true>(bf16, d, bs, a, mk, mv, grid, s);
       case pkv::kSuffix: return run_decode_mode<pkv::kSuffix, true>(bf16, d, bs, a, mk, mv, grid, s);
       case pkv::kAppend: return run_decode_mode<pkv::kAppend, true>(bf16, d, bs, a, mk, mv, grid, s);
+      case pkv::kWindow: return run_decode_mode<pkv::kWindow, true>(bf16, d, bs, a, mk, mv, grid, s);
     }
     return PA_ERR_INVALID;
   }
@@ -169,6 +175,7 @@ pa_status dispatch_mode(bool kv8, bool wide, int mode, bool bf16, int d, int bs,
     case pkv::kPrefix: return run_decode_mode<pkv::kPrefix, false>(bf16, d, bs, a, mk, mv, grid, s);
     case pkv::kSuffix: return run_decode_mode<pkv::kSuffix, false>(bf16, d, bs, a, mk, mv, grid, s);
     case pkv::kAppend: return run_decode_mode<pkv::kAppend, false>(bf16, d, bs, a, mk, mv, grid, s);
+    case pkv::kWindow: return run_decode_mode<pkv::kWindow, false>(bf16, d, bs, a, mk, mv, grid, s);
   }
   return PA_ERR_INVALID;
 }
@@ -189,6 +196,7 @@ struct CascadeArgs {
   const float* k_bscale = nullptr;   // 8-bit caches: per-(block, kv head) scales instead
   const float* v_bscale = nullptr;
   int max_grid = 0;              // > 0: at most this many CTAs (one per segment)
+  int window = 0, num_sinks = 0; // kWindow
 };
 
 // Validation, workspace layout, tensor maps and launch shared by the decode entry points.
@@ -212,9 +220,11 @@ pa_status decode_impl(void* out, const void* q, const void* k_cache, const void*
   // query columns per kv head: up to 16 on the mma.sync kernel (every mode), up to 64 on
   // the tcgen05 kernel (16-bit pools: plain, prefix and fused-append modes)
   const bool wide_mode = !cx.kv8 && (cx.mode == pkv::kPlain || cx.mode == pkv::kPrefix ||
-                                     cx.mode == pkv::kAppend);
+                                     cx.mode == pkv::kAppend || cx.mode == pkv::kWindow);
   if (ncol > (wide_mode ? pkv::kWideCols : pkv::kMaxGroup)) return PA_ERR_UNSUPPORTED;
-  const bool wide = wide_mode && ncol >= wide_min_cols();
+  if (cx.mode == pkv::kWindow && (cx.window < 1 || cx.num_sinks < 0)) return PA_ERR_INVALID;
+  // (the window's mma.sync instances hold up to 8 query columns, whatever the override says)
+  const bool wide = wide_mode && ncol >= (cx.mode == pkv::kWindow ? 9 : wide_min_cols());
   if ((long long)num_blocks * num_kv_heads * block_size >= (1ll << 31) ||
       (long long)max_blocks_per_seq * block_size >= (1ll << 31) ||
       (long long)num_seqs * num_kv_heads >= (1ll << 31))
@@ -293,6 +303,9 @@ pa_status decode_impl(void* out, const void* q, const void* k_cache, const void*
   a.late_wait = cx.late_wait;
   a.k_bscale = cx.k_bscale;
   a.v_bscale = cx.v_bscale;
+  // no position is further back than ctx_cap: larger windows and more first tokens see the same
+  a.window = std::min(cx.window, a.ctx_cap);
+  a.num_sinks = std::min(cx.num_sinks, a.ctx_cap);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return dispatch_mode(cx.kv8, wide, cx.mode, dtype == PA_BF16, head_dim, block_size, a, mk, mv,
                        grid, st);
@@ -424,6 +437,44 @@ pa_status pa_decode_multi(void* out, const void* q, const void* k_cache, const v
                      num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
                      num_blocks, scale, dtype, workspace, workspace_bytes, 0, dev_status,
                      stream);
+}
+
+pa_status pa_decode_window(void* out, const void* q, const void* k_cache, const void* v_cache,
+                           const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                           int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                           int block_size, int max_blocks_per_seq, int num_blocks, int window,
+                           int num_sinks, float scale, pa_dtype dtype, void* workspace,
+                           size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  CascadeArgs cx;
+  cx.mode = pkv::kWindow;
+  cx.window = window;
+  cx.num_sinks = num_sinks;
+  return decode_impl(out, q, k_cache, v_cache, block_tables, context_lens, num_seqs, q_len,
+                     num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                     num_blocks, scale, dtype, workspace, workspace_bytes, 0, dev_status, stream,
+                     cx);
+}
+
+pa_status pa_decode_window_e4m3_bs(void* out, const void* q, const void* k_cache,
+                                   const void* v_cache, const float* k_scales,
+                                   const float* v_scales, const int32_t* block_tables,
+                                   const int32_t* context_lens, int num_seqs, int q_len,
+                                   int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                   int max_blocks_per_seq, int num_blocks, int window,
+                                   int num_sinks, float scale, pa_dtype dtype, void* workspace,
+                                   size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  if (num_seqs > 0 && (!k_scales || !v_scales)) return PA_ERR_INVALID;
+  CascadeArgs cx;
+  cx.mode = pkv::kWindow;
+  cx.window = window;
+  cx.num_sinks = num_sinks;
+  cx.kv8 = true;
+  cx.k_bscale = k_scales;
+  cx.v_bscale = v_scales;
+  return decode_impl(out, q, k_cache, v_cache, block_tables, context_lens, num_seqs, q_len,
+                     num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                     num_blocks, scale, dtype, workspace, workspace_bytes, 0, dev_status, stream,
+                     cx);
 }
 
 pa_status pa_decode_append(void* out, const void* q, void* k_cache, void* v_cache,
@@ -694,6 +745,133 @@ pa_status pa_copy_blocks(void* const* k_caches, void* const* v_caches, int num_l
       return PA_ERR_CUDA;
   }
   return PA_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Arguments shared by the two compaction calls; elem_bytes 1 or 2.
+pa_status compact_args(pkv::CompactArgs& a, void* const* k_caches, void* const* v_caches,
+                       int num_layers, const int32_t* src_tables, int src_blocks_per_seq,
+                       const int32_t* dst_tables, int dst_blocks_per_seq,
+                       const int32_t* context_lens, const int32_t* keep, const int32_t* keep_lens,
+                       int max_keep, int keep_per_layer, int keep_per_head, int num_seqs,
+                       int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                       int32_t* dev_status) {
+  if (num_layers < 0 || num_seqs < 0 || num_kv_heads <= 0 || src_blocks_per_seq <= 0 ||
+      dst_blocks_per_seq <= 0 || max_keep < 0 || num_blocks <= 0)
+    return PA_ERR_INVALID;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (block_size != 1 && block_size != 8 && block_size != 16 && block_size != 32)
+    return PA_ERR_UNSUPPORTED;
+  if ((long long)num_blocks * num_kv_heads * block_size >= (1ll << 31) ||
+      (long long)src_blocks_per_seq * block_size >= (1ll << 31) ||
+      (long long)dst_blocks_per_seq * block_size >= (1ll << 31) ||
+      (long long)num_seqs * num_kv_heads >= (1ll << 31))
+    return PA_ERR_INVALID;
+  if (num_layers == 0 || num_seqs == 0 || max_keep == 0) return PA_OK;
+  if (!k_caches || !v_caches || !src_tables || !dst_tables || !context_lens || !keep || !keep_lens)
+    return PA_ERR_INVALID;
+  for (int l = 0; l < num_layers; ++l)
+    if (!k_caches[l] || !v_caches[l] || !aligned16(k_caches[l]) || !aligned16(v_caches[l]))
+      return PA_ERR_INVALID;
+  a.src_tables = src_tables;
+  a.dst_tables = dst_tables;
+  a.context_lens = context_lens;
+  a.keep = keep;
+  a.keep_lens = keep_lens;
+  a.status = dev_status;
+  a.src_width = src_blocks_per_seq;
+  a.dst_width = dst_blocks_per_seq;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.max_keep = max_keep;
+  a.keep_head = keep_per_head ? max_keep : 0;
+  a.keep_seq = (long long)max_keep * (keep_per_head ? num_kv_heads : 1);
+  a.keep_layer = keep_per_layer ? a.keep_seq * num_seqs : 0;
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_compact_tokens(void* const* k_caches, void* const* v_caches, int num_layers,
+                            const int32_t* src_tables, int src_blocks_per_seq,
+                            const int32_t* dst_tables, int dst_blocks_per_seq,
+                            const int32_t* context_lens, const int32_t* keep,
+                            const int32_t* keep_lens, int max_keep, int keep_per_layer,
+                            int keep_per_head, int num_seqs, int num_kv_heads, int head_dim,
+                            int elem_bytes, int block_size, int num_blocks, int32_t* dev_status,
+                            void* stream) {
+  if (elem_bytes != 1 && elem_bytes != 2) return PA_ERR_UNSUPPORTED;
+  pkv::CompactArgs a{};
+  const pa_status r = compact_args(a, k_caches, v_caches, num_layers, src_tables,
+                                   src_blocks_per_seq, dst_tables, dst_blocks_per_seq,
+                                   context_lens, keep, keep_lens, max_keep, keep_per_layer,
+                                   keep_per_head, num_seqs, num_kv_heads, head_dim, block_size,
+                                   num_blocks, dev_status);
+  if (r != PA_OK) return r;
+  if (num_layers == 0 || num_seqs == 0 || max_keep == 0) return PA_OK;
+  const int cpr = head_dim * elem_bytes / 16;
+  for (int l0 = 0; l0 < num_layers; l0 += pkv::kMaxLayersPerLaunch) {
+    const int n = std::min(num_layers - l0, pkv::kMaxLayersPerLaunch);
+    pkv::LayerPtrs P;
+    std::memset(&P, 0, sizeof(P));
+    for (int i = 0; i < n; ++i) {
+      P.k[i] = static_cast<uint4*>(k_caches[l0 + i]);
+      P.v[i] = static_cast<uint4*>(v_caches[l0 + i]);
+    }
+    auto kernel = cpr == 4 ? pkv::pa_compact_kernel<4>
+                           : (cpr == 8 ? pkv::pa_compact_kernel<8> : pkv::pa_compact_kernel<16>);
+    if (pkv_host::launch(kernel, dim3((unsigned)(num_seqs * num_kv_heads), (unsigned)(2 * n)),
+                         dim3(pkv::kCompactThreads), 0, static_cast<cudaStream_t>(stream), P, a,
+                         l0) != cudaSuccess)
+      return PA_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_compact_tokens_e4m3_bs(void* const* k_caches, void* const* v_caches,
+                                    float* const* k_scales, float* const* v_scales,
+                                    int num_layers, const int32_t* src_tables,
+                                    int src_blocks_per_seq, const int32_t* dst_tables,
+                                    int dst_blocks_per_seq, const int32_t* context_lens,
+                                    const int32_t* keep, const int32_t* keep_lens, int max_keep,
+                                    int keep_per_layer, int keep_per_head, int num_seqs,
+                                    int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                    int32_t* dev_status, void* stream) {
+  pkv::CompactArgs a{};
+  const pa_status r = compact_args(a, k_caches, v_caches, num_layers, src_tables,
+                                   src_blocks_per_seq, dst_tables, dst_blocks_per_seq,
+                                   context_lens, keep, keep_lens, max_keep, keep_per_layer,
+                                   keep_per_head, num_seqs, num_kv_heads, head_dim, block_size,
+                                   num_blocks, dev_status);
+  if (r != PA_OK) return r;
+  if (num_layers == 0 || num_seqs == 0 || max_keep == 0) return PA_OK;
+  if (!k_scales || !v_scales) return PA_ERR_INVALID;
+  for (int l = 0; l < num_layers; ++l)
+    if (!k_scales[l] || !v_scales[l]) return PA_ERR_INVALID;
+  for (int l0 = 0; l0 < num_layers; l0 += pkv::kScaledLayersPerLaunch) {
+    const int n = std::min(num_layers - l0, pkv::kScaledLayersPerLaunch);
+    pkv::ScaledLayerPtrs P;
+    std::memset(&P, 0, sizeof(P));
+    for (int i = 0; i < n; ++i) {
+      P.k[i] = static_cast<uint4*>(k_caches[l0 + i]);
+      P.v[i] = static_cast<uint4*>(v_caches[l0 + i]);
+      P.ks[i] = k_scales[l0 + i];
+      P.vs[i] = v_scales[l0 + i];
+    }
+    auto kernel = head_dim == 64 ? pkv::pa_compact_e4m3_bs_kernel<4>
+                                 : pkv::pa_compact_e4m3_bs_kernel<8>;
+    if (pkv_host::launch(kernel, dim3((unsigned)(num_seqs * num_kv_heads), (unsigned)(2 * n)),
+                         dim3(pkv::kCompactThreads), 0, static_cast<cudaStream_t>(stream), P, a,
+                         l0) != cudaSuccess)
+      return PA_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status pa_check_bounded_waits(int32_t* result, int limit_us, void* stream) {

@@ -1,0 +1,230 @@
+// compact.cuh -- the kept tokens of a sequence moved to the front of its pages.
+//
+// Row i of the new sequence is row keep[i] of the old one (keep ascending), for every kv
+// head of every layer's K and V pool.  Old rows are read through the source table, new ones
+// written through the destination table; the two may name the same blocks (in place).
+//
+// What bounds it: every kept row is read and written once, nothing is computed, so HBM.  A
+// row is 64 to 256 bytes at an arbitrary place, so the loads are 16 bytes a lane with a
+// row's lanes side by side (whole 32-byte sectors) and what hides their latency is bytes in
+// flight: kU loads a thread and several CTAs an SM.
+//
+// In place, writing new rows [i0, i1) overwrites old rows that only new rows j <= keep[j] <
+// i1 take.  So one CTA walks a (sequence, kv head, pool) list front to back in chunks and
+// the one condition is that all loads of a chunk are done before its first store: one
+// barrier a chunk.  Lists of different sequences, heads, layers and pools share no byte that
+// is written, so they need no order.
+#pragma once
+#include <cstdint>
+
+#include "decode.cuh"
+#include "kv_ops.cuh"
+
+namespace pkv {
+
+constexpr int DEV_BAD_KEEP = 0x20;
+constexpr int kCompactThreads = 256;
+constexpr int kScaledLayersPerLaunch = 64;        // pointers of this many layers a launch
+
+struct CompactArgs {
+  const int32_t* src_tables;      // [num_seqs][src_width]
+  const int32_t* dst_tables;      // [num_seqs][dst_width]
+  const int32_t* context_lens;    // [num_seqs]
+  const int32_t* keep;            // [layer][seq][head][max_keep] by the strides below
+  const int32_t* keep_lens;       // [num_seqs]
+  int32_t* status;                // nullable
+  int src_width, dst_width, num_kv_heads, block_size, num_blocks, max_keep;
+  long long keep_layer, keep_seq, keep_head;      // strides in elements (0: shared)
+};
+
+struct ScaledLayerPtrs {
+  uint4* k[kScaledLayersPerLaunch];
+  uint4* v[kScaledLayersPerLaunch];
+  float* ks[kScaledLayersPerLaunch];
+  float* vs[kScaledLayersPerLaunch];
+};
+
+// Kept rows of sequence s, and its old length, both clamped to what the tables hold.
+__device__ __forceinline__ int compact_rows(const CompactArgs& a, int s, int& ctx, bool report) {
+  ctx = clamp_ctx(a.context_lens[s], a.src_width * a.block_size, report ? a.status : nullptr);
+  int n = a.keep_lens[s];
+  const int cap = min(a.max_keep, a.dst_width * a.block_size);
+  if (n < 0 || n > cap) {
+    if (report && a.status) atomicOr(a.status, DEV_BAD_KEEP);
+    n = n < 0 ? 0 : cap;
+  }
+  return n;
+}
+
+// Old and new row (block, kv head, offset) of kept row i; false (and a status bit) when the
+// position or a block id is out of range.
+__device__ __forceinline__ bool compact_row(const CompactArgs& a, const int32_t* keep, int s,
+                                            int h, int ctx, int i, long long& src,
+                                            long long& dst) {
+  const int t = __ldg(keep + i);
+  if (t < 0 || t >= ctx) {
+    if (a.status) atomicOr(a.status, DEV_BAD_KEEP);
+    return false;
+  }
+  const int bs = a.block_size;
+  const int sb = __ldg(a.src_tables + (long long)s * a.src_width + t / bs);
+  const int db = __ldg(a.dst_tables + (long long)s * a.dst_width + i / bs);
+  if ((unsigned)sb >= (unsigned)a.num_blocks || (unsigned)db >= (unsigned)a.num_blocks) {
+    if (a.status) atomicOr(a.status, DEV_BAD_BLOCK_ID);
+    return false;
+  }
+  src = ((long long)sb * a.num_kv_heads + h) * bs + t % bs;
+  dst = ((long long)db * a.num_kv_heads + h) * bs + i % bs;
+  return true;
+}
+
+// Rows moved byte for byte (16-bit pools, 8-bit pools with one scale per pool).  CPR: 16-byte
+// pieces per row.  grid = (sequences * kv heads, layers * 2 pools).
+template <int CPR>
+__global__ void __launch_bounds__(kCompactThreads)
+    pa_compact_kernel(const __grid_constant__ LayerPtrs P, const CompactArgs a, int layer0) {
+  constexpr int kU = 8;                                   // 16-byte loads a thread and chunk
+  constexpr int kRows = kCompactThreads * kU / CPR;       // rows of a chunk
+  constexpr int kPer = (kRows + kCompactThreads - 1) / kCompactThreads;
+  // places of three chunks (-1: nothing to move): chunk c + 1's are found while the slowest
+  // warp may still be storing chunk c - 1
+  __shared__ long long src_s[3][kRows], dst_s[3][kRows];
+  pdl_wait();
+  pdl_trigger();
+  const int s = blockIdx.x / a.num_kv_heads, h = blockIdx.x % a.num_kv_heads;
+  const int layer = blockIdx.y >> 1, pool = blockIdx.y & 1;
+  const int tid = threadIdx.x;
+  int ctx;
+  const int n = compact_rows(a, s, ctx, h == 0 && blockIdx.y == 0 && tid == 0);
+  const int32_t* keep = a.keep + (layer0 + layer) * a.keep_layer + s * a.keep_seq + h * a.keep_head;
+  uint4* base = pool ? P.v[layer] : P.k[layer];
+  auto places = [&](int c) {                              // rows of chunk c -> src_s, dst_s
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int r = tid + k * kCompactThreads, i = c * kRows + r;
+      if (r >= kRows) break;
+      long long src = -1, dst = -1;
+      if (i < n && (!compact_row(a, keep, s, h, ctx, i, src, dst) || src == dst)) src = dst = -1;
+      src_s[c % 3][r] = src;
+      dst_s[c % 3][r] = dst;
+    }
+  };
+  const int nc = (n + kRows - 1) / kRows;
+  if (nc) places(0);
+  __syncthreads();
+  for (int c = 0; c < nc; ++c) {
+    uint4 x[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int e = u * kCompactThreads + tid;
+      const long long src = src_s[c % 3][e / CPR];
+      if (src >= 0) x[u] = *(base + src * CPR + e % CPR);
+    }
+    if (c + 1 < nc) places(c + 1);
+    __syncthreads();                                      // every load of the chunk is done
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int e = u * kCompactThreads + tid;
+      const long long dst = dst_s[c % 3][e / CPR];
+      if (dst >= 0) *(base + dst * CPR + e % CPR) = x[u];
+    }
+  }
+}
+
+// 8-bit (E4M3) pools with per-(block, kv head) scales: a kept row's values are scale * code of
+// its old block; a new block's scale is the one that its first row fixes (e4m3_block_scale of
+// that row's largest magnitude, the rule of the append), and every row of the block is
+// quantised with it.  The powers of two make value / scale exact, so a code changes only
+// where the scale grew past its low bits or shrank below its magnitude.
+template <int CPR>
+__global__ void __launch_bounds__(kCompactThreads)
+    pa_compact_e4m3_bs_kernel(const __grid_constant__ ScaledLayerPtrs P, const CompactArgs a,
+                              int layer0) {
+  constexpr int kU = 4;
+  constexpr int kRows = kCompactThreads * kU / CPR;       // a multiple of every block size
+  static_assert(kRows % 32 == 0, "a chunk holds whole blocks");
+  constexpr int kPer = (kRows + kCompactThreads - 1) / kCompactThreads;
+  __shared__ long long src_s[3][kRows], dst_s[3][kRows];
+  __shared__ float new_s[2][kRows];                       // a chunk's new block scales
+  pdl_wait();
+  pdl_trigger();
+  const int s = blockIdx.x / a.num_kv_heads, h = blockIdx.x % a.num_kv_heads;
+  const int layer = blockIdx.y >> 1, pool = blockIdx.y & 1;
+  const int tid = threadIdx.x, bs = a.block_size;
+  int ctx;
+  const int n = compact_rows(a, s, ctx, h == 0 && blockIdx.y == 0 && tid == 0);
+  const int32_t* keep = a.keep + (layer0 + layer) * a.keep_layer + s * a.keep_seq + h * a.keep_head;
+  uint4* base = pool ? P.v[layer] : P.k[layer];
+  float* scales = pool ? P.vs[layer] : P.ks[layer];
+  auto places = [&](int c) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int r = tid + k * kCompactThreads, i = c * kRows + r;
+      if (r >= kRows) break;
+      long long src = -1, dst = -1;
+      if (i < n && !compact_row(a, keep, s, h, ctx, i, src, dst)) src = dst = -1;
+      src_s[c % 3][r] = src;
+      dst_s[c % 3][r] = dst;
+    }
+  };
+  const int nc = (n + kRows - 1) / kRows;
+  if (nc) places(0);
+  __syncthreads();
+  for (int c = 0; c < nc; ++c) {
+    uint4 x[kU];
+    float sc[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int e = u * kCompactThreads + tid;
+      const long long src = src_s[c % 3][e / CPR];
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      sc[u] = 1.f;
+      if (src >= 0) {
+        x[u] = *(base + src * CPR + e % CPR);
+        sc[u] = scales[src / bs];                         // row / bs = block * heads + head
+      }
+    }
+    if (c + 1 < nc) places(c + 1);
+    // the first row of each new block fixes its scale
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int r = (u * kCompactThreads + tid) / CPR;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[u]);
+      float am = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t lo, hi;
+        e4m3x4_to_f16x2x2(w[k], lo, hi);
+        const float2 f0 = unpack2<__half>(lo), f1 = unpack2<__half>(hi);
+        am = fmaxf(am, fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))));
+      }
+#pragma unroll
+      for (int o = 1; o < CPR; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+      if (r % bs == 0 && tid % CPR == 0) new_s[c & 1][r / bs] = e4m3_block_scale(am * sc[u]);
+    }
+    __syncthreads();                                      // loads done, new scales known
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int e = u * kCompactThreads + tid;
+      const int r = e / CPR;
+      const long long dst = dst_s[c % 3][r];
+      if (dst < 0) continue;
+      const float ns = new_s[c & 1][r / bs];
+      const float inv = 1.f / ns;                         // a power of two: exact
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[u]);
+      uint32_t q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t lo, hi;
+        e4m3x4_to_f16x2x2(w[k], lo, hi);
+        const float2 f0 = unpack2<__half>(lo), f1 = unpack2<__half>(hi);
+        q[k] = f32x2_to_e4m3x2(f0.x * sc[u] * inv, f0.y * sc[u] * inv) |
+               (f32x2_to_e4m3x2(f1.x * sc[u] * inv, f1.y * sc[u] * inv) << 16);
+      }
+      *(base + dst * CPR + e % CPR) = make_uint4(q[0], q[1], q[2], q[3]);
+      if (r % bs == 0 && e % CPR == 0) scales[dst / bs] = ns;
+    }
+  }
+}
+
+}  // namespace pkv

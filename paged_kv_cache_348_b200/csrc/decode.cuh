@@ -100,7 +100,11 @@ enum : int { F_FIRST = 1, F_LAST = 2, F_END = 4, F_COMPLETE = 8, F_PREFIX = 16 }
 //              the external partial of its prefix when seq_start[s] > 0.
 //  kAppend  -- kPlain with one new token per sequence whose K/V (k_new, v_new) are patched
 //              into the tiles and written to the cache in the same launch.
-enum : int { kPlain = 0, kPrefix = 1, kSuffix = 2, kAppend = 3 };
+//  kWindow  -- kPlain with a sliding window and visible first tokens: the new token at
+//              position p sees the positions t <= p with t > p - window or t < num_sinks.
+//              A segment is the units of the first tokens and then those of the window
+//              (WinSpan below); what lies between is neither scheduled nor read.
+enum : int { kPlain = 0, kPrefix = 1, kSuffix = 2, kAppend = 3, kWindow = 4 };
 
 struct StageMeta {
   int seq, kvh, tok0, nunits, ctx, flags, pidx, qslot;
@@ -152,7 +156,49 @@ struct DecodeArgs {
   // 8-bit caches with per-(block, kv head) scales [num_blocks][Hkv] (null: per-tensor)
   const float* k_bscale;
   const float* v_bscale;
+  int window, num_sinks;        // kWindow (both at most ctx_cap)
 };
+
+// kWindow: which cached tokens of a sequence some new token sees.  Position t < ctx is seen
+// when t >= w0 (the start of the oldest new token's window) or t < num_sinks.  The schedule
+// lays the sequence out as "virtual" tokens: the head units (the first tokens, rounded up
+// to 16) and, right behind them, the units from the one holding w0 on; virtual token v is
+// position v below `head` and v + jump from there, so a 16-token unit is always 16
+// consecutive positions.
+struct WinSpan {
+  int ctx, w0, sinks, head, jump;
+  __device__ __forceinline__ int pos(int v) const { return v < head ? v : v + jump; }
+  __device__ __forceinline__ int vctx() const { return ctx - jump; }   // virtual tokens
+  __device__ __forceinline__ bool seen(int t) const { return t < ctx && (t >= w0 || t < sinks); }
+  // whether any of the positions t .. t + n - 1 is seen
+  __device__ __forceinline__ bool any_seen(int t, int n) const {
+    return t < ctx && (t + n > w0 || t < sinks);
+  }
+  // bit r: position t + r is seen, r < 16
+  __device__ __forceinline__ uint32_t seen16(int t) const {
+    auto below = [](int n) { return n <= 0 ? 0u : (n >= 16 ? 0xffffu : (1u << n) - 1u); };
+    return below(ctx - t) & (~below(w0 - t) | below(sinks - t));
+  }
+};
+__device__ __forceinline__ WinSpan win_span(const DecodeArgs& a, int ctx) {
+  WinSpan w;
+  w.ctx = ctx;
+  const long long first = (long long)ctx - a.q_len - a.window + 1;
+  w.w0 = first > 0 ? (int)first : 0;
+  w.sinks = a.num_sinks;
+  const int wu = w.w0 / kUnit * kUnit;             // the window's first unit
+  // the first tokens' units, short of the window's (whose rows below num_sinks are seen too)
+  const int hu = a.num_sinks < wu ? (a.num_sinks + kUnit - 1) / kUnit * kUnit : wu;
+  w.head = hu < wu ? hu : wu;
+  w.jump = wu - w.head;
+  return w;
+}
+// Schedule units of a sequence whose span is (ctx, first).
+template <int MODE>
+__device__ __forceinline__ int seq_units(const DecodeArgs& a, int ctx, int first) {
+  if constexpr (MODE == kWindow) ctx = win_span(a, ctx).vctx();
+  return (ctx - first + kUnit - 1) / kUnit;
+}
 
 
 // Shared-memory layout of a CTA.  16-bit caches: K and V tiles of 64 tokens in D/64
@@ -488,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
   constexpr int kSegW = seg_weight(BS);
   static_assert(!KV8 || D == 128 || D == 64, "8-bit caches: head_dim 128 or 64");
   static_assert(!KV8 || MODE == kPlain || KSC,
-                "8-bit caches: the cascade and fused-append modes use per-block scales");
+                "8-bit caches: the cascade, fused-append and window modes use per-block scales");
   static_assert(!KSC || KV8, "per-block scales belong to 8-bit caches");
   static_assert(ctas_per_sm(KV8, NT, BS) == 2 || NT == 1, "the 3-CTA layout holds 8 columns");
   // MMA operand type: the cache's 16-bit type, or fp16 for E4M3 (exact there)
@@ -565,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
       SeqSpan sp{0, 0};
       if (s < B) sp = span_of<MODE>(a, s, c == 0 ? a.status : nullptr);
       const int ctx = sp.ctx;
-      const int u = (ctx - sp.first + kUnit - 1) / kUnit;
+      const int u = seq_units<MODE>(a, ctx, sp.first);
       int x = u ? u + kSegW : 0;                     // weight of each of its segments
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -605,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
           if (s < B) sp = span_of<MODE>(a, s, nullptr);
           ctx = sp.ctx;
           first = sp.first;
-          u = (ctx - first + kUnit - 1) / kUnit;
+          u = seq_units<MODE>(a, ctx, first);
           x = u ? u + kSegW : 0;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -657,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
           const SeqSpan sp = span_of<MODE>(a, s_cur, nullptr);
           ctx_cur = sp.ctx;
           if constexpr (MODE == kSuffix) first_cur = sp.first;
-          u_cur = (ctx_cur - first_cur + kUnit - 1) / kUnit;
+          u_cur = seq_units<MODE>(a, ctx_cur, first_cur);
         }
         const int w_cur = u_cur + kSegW;
         const int kvh = (int)((x - pbase) / w_cur);
@@ -689,7 +735,31 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
         int wb = (first_cur + (int)(x - seg0) * kUnit) / BS;
         const int32_t* trow;
         int w0, w1, n0, n1, m0 = -1, m1 = -1, p0 = -1, p1 = -1;
-        if (x == seg0 && s_cur == s_win) {            // warp-uniform
+        // kWindow: the positions jump once in a segment, so there is no register window; a
+        // lane reads the entries of its own box (block_size 1: of its two rows) one stage
+        // ahead
+        [[maybe_unused]] WinSpan win{};
+        [[maybe_unused]] int e0 = -1, e1 = -1;
+        [[maybe_unused]] auto entries = [&](long long tu) {
+          const int v0 = (int)(tu - seg0) * kUnit;
+          auto entry = [&](int v, int n) {             // the block of positions pos(v) ..
+            const int t = win.pos(v);
+            return win.any_seen(t, n) ? __ldg(trow + t / BS) : -1;
+          };
+          if constexpr (BS == 1) {
+            e0 = entry(v0 + lane, 1);
+            e1 = entry(v0 + 32 + lane, 1);
+          } else {
+            constexpr int H = BS < 16 ? BS : 16;
+            e0 = entry(v0 + (lane >> 1) / (KV8 ? 1 : L::kHalves) * H, H);
+          }
+        };
+        if constexpr (MODE == kWindow) {
+          trow = a.block_tables + (long long)s_cur * a.max_blocks;
+          w0 = w1 = n0 = n1 = -1;
+          win = win_span(a, ctx_cur);
+          entries(x);
+        } else if (x == seg0 && s_cur == s_win) {     // warp-uniform
           trow = s_trow;
           w0 = sw0;
           w1 = sw1;
@@ -734,7 +804,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
         for (long long tu = x; tu < pe; tu += kUnitsPerStage) {
           const int nun = (int)((pe - tu) < kUnitsPerStage ? (pe - tu) : kUnitsPerStage);
           const int tok0 = first_cur + (int)(tu - seg0) * kUnit;
-          if (tok0 / BS >= wb + 64) {                 // warp-uniform: slide the window
+          [[maybe_unused]] int c0 = e0, c1 = e1;      // kWindow: this stage's entries
+          if constexpr (MODE == kWindow) {
+            if (tu + kUnitsPerStage < pe) entries(tu + kUnitsPerStage);
+          } else if (tok0 / BS >= wb + 64) {          // warp-uniform: slide the window
             w0 = n0;
             w1 = n1;
             wb += 64;
@@ -811,13 +884,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
             const int hf = (lane >> 1) % kParts;
             const int jb = (lane >> 1) / kParts;
             const int j = jb / BPU, b = jb % BPU;
-            const int t = tok0 + j * kUnit + b * H;
-            const bool mine = lane < nbox && t < ctx_cur;
+            const int tv = tok0 + j * kUnit + b * H;
+            const int t = MODE == kWindow ? win.pos(tv) : tv;
+            const bool mine = lane < nbox && (MODE == kWindow ? win.any_seen(t, H) : t < ctx_cur);
             // the stage spans blocks tok0/BS .. +64/BS-1 < wb + 72: w0, w1 and, only when it
             // runs past the window, n0 (whose load was issued 64 blocks ago)
             const int wi = mine ? t / BS - wb : 0;
             int blk;
-            if ((tok0 + kTileTokens - 1) / BS >= wb + 64)   // warp-uniform
+            if constexpr (MODE == kWindow)
+              blk = c0;
+            else if ((tok0 + kTileTokens - 1) / BS >= wb + 64)   // warp-uniform
               blk = win_lookup(w0, w1, n0, wi);
             else
               blk = win_lookup(w0, w1, w1, wi);       // never touches n0 while it loads
@@ -833,7 +909,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
               }
             }
             uint32_t bytes = qbytes + nbytes;
-            for (int jj = 0; jj < nun; ++jj) {
+            if constexpr (MODE == kWindow)
+              bytes += (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * kBoxBytes);
+            else for (int jj = 0; jj < nun; ++jj) {
               const int rem = ctx_cur - (tok0 + jj * kUnit);
               const int nb = (rem + H - 1) / H;
               bytes += (uint32_t)((nb < BPU ? nb : BPU) * kBoxBytes * kParts * 2);
@@ -880,11 +958,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
             // this stage's table entries, handed out by shuffle.
             constexpr int kParts = kGParts, kPieceB = kGPieceB;
             const int ntok = nun * kUnit;
+            if constexpr (MODE == kWindow) {           // -1: a row that nothing sees
+              w0 = c0;
+              w1 = c1;
+            }
+            const int vctx = MODE == kWindow ? win.vctx() : ctx_cur;   // tokens as scheduled
             // KSC: the K / V scales of rows lane and 32+lane (this stage's table entries
             // are w0, w1), read before the slot wait
             float sck0 = 0.f, sck1 = 0.f, scv0 = 0.f, scv1 = 0.f;
             if constexpr (KSC) {
-              const int nv = ntok < ctx_cur - tok0 ? ntok : ctx_cur - tok0;
+              const int nv = ntok < vctx - tok0 ? ntok : vctx - tok0;
               if (lane < nv && (unsigned)w0 < (unsigned)a.num_blocks) {
                 sck0 = __ldg(a.k_bscale + w0 * Hkv + kvh);
                 scv0 = __ldg(a.v_bscale + w0 * Hkv + kvh);
@@ -912,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
             // load items: (group of 4 rows g, piece hf, pool kv), at most 16 * 2 * 2 = 64,
             // two a lane; rows past the valid tokens (or with a bad block id) read row
             // rows_total, out of range, which the TMA fills with zeros
-            const int nvalid = ntok < ctx_cur - tok0 ? ntok : ctx_cur - tok0;
+            const int nvalid = ntok < vctx - tok0 ? ntok : vctx - tok0;
             const int nitems = ((nvalid + 3) >> 2) * kParts * 2;
             static_assert(kTileTokens / 4 * kParts * 2 <= 64, "two load items a lane");
             if (lane == 0) {
@@ -931,7 +1014,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
               int y = rows_total;
               if (r < nvalid) {
                 if ((unsigned)blk < (unsigned)a.num_blocks) y = blk * Hkv + kvh;
-                else if (a.status) atomicOr(a.status, DEV_BAD_BLOCK_ID);
+                else if (a.status && (MODE != kWindow || win.seen(win.pos(tok0 + r))))
+                  atomicOr(a.status, DEV_BAD_BLOCK_ID);
               }
               yc[r] = y;
             }
@@ -1113,8 +1197,24 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
     for (int uk = 0; uk < UPW; ++uk) {
       const int u = kColSplit ? (cw >> 1) * 2 + uk : cw;   // unit of the stage
       if (u < mt.nunits) {
-        const int t0 = mt.tok0 + u * kUnit;
+        int t0 = mt.tok0 + u * kUnit;
+        [[maybe_unused]] WinSpan win{};
+        if constexpr (MODE == kWindow) {
+          win = win_span(a, mt.ctx);
+          t0 = win.pos(t0);
+        }
         const int valid = (mt.ctx - t0) < kUnit ? (mt.ctx - t0) : kUnit;
+        // kWindow: the rows of the unit that some new token sees, and the rows, counted
+        // from the unit's start, where new token 0's window begins and the first tokens end
+        const uint32_t seen = MODE == kWindow ? win.seen16(t0) : 0xffffu;
+        [[maybe_unused]] int wlo = 0, sk = 0;
+        if constexpr (MODE == kWindow) {
+          const long long lo = (long long)mt.ctx - a.q_len - a.window + 1 - t0;
+          wlo = lo < -1024 ? -1024 : (int)lo;
+          sk = a.num_sinks - t0;
+        }
+        const bool whole = MODE == kWindow ? seen == 0xffffu : valid == kUnit;
+        auto row_in = [&](int r) { return MODE == kWindow ? (seen >> r & 1u) != 0u : r < valid; };
         // causal limit: new token j sees unit rows < ctx - q_len + 1 + j - t0 (a prefix
         // launch's columns are different sequences: no mask)
         const int lim0 = MODE == kPrefix ? (1 << 30) : mt.ctx - a.q_len + 1 - t0;
@@ -1244,8 +1344,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
           sl_hi = a.scale_log2 * sc[r0 + 8];
           // a row past the valid tokens has p = 0; its scale may be that of a block whose
           // offset 0 was never written (anything, NaN included), so it must not reach P
-          vs_lo = gid < valid ? sc[kTileTokens + r0] : 0.f;
-          vs_hi = gid + 8 < valid ? sc[kTileTokens + r0 + 8] : 0.f;
+          vs_lo = row_in(gid) ? sc[kTileTokens + r0] : 0.f;
+          vs_hi = row_in(gid + 8) ? sc[kTileTokens + r0 + 8] : 0.f;
         }
         uint32_t bhi[NTW][2], blo[NTW][2];
 #pragma unroll
@@ -1255,7 +1355,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
           for (int e = 0; e < 4; ++e) {
             const int row = gid + (e >= 2 ? 8 : 0);
             const int lim = lim0 + jcol[n][e & 1];
-            xs[e] = (row < valid && row < lim) ? sacc[n][e] * (e >= 2 ? sl_hi : sl_lo) : -INFINITY;
+            bool see = row < valid && row < lim;
+            if constexpr (MODE == kWindow) see = see && (row >= wlo + jcol[n][e & 1] || row < sk);
+            xs[e] = see ? sacc[n][e] * (e >= 2 ? sl_hi : sl_lo) : -INFINITY;
           }
           float alpha[2], p[4];
           bool grew = false;
@@ -1303,11 +1405,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
           }
         }
         // ---- O^T[D][8*NT] += V_unit^T . P^T
-        uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;   // token masks for V rows >= valid
-        if (valid < kUnit) {
+        uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;   // token masks for V rows not in play
+        if (!whole) {
           const int t_a = 2 * tig, t_b = 8 + 2 * tig;
-          mlo = (t_a < valid ? 0x0000ffffu : 0u) | (t_a + 1 < valid ? 0xffff0000u : 0u);
-          mhi = (t_b < valid ? 0x0000ffffu : 0u) | (t_b + 1 < valid ? 0xffff0000u : 0u);
+          mlo = (row_in(t_a) ? 0x0000ffffu : 0u) | (row_in(t_a + 1) ? 0xffff0000u : 0u);
+          mhi = (row_in(t_b) ? 0x0000ffffu : 0u) | (row_in(t_b + 1) ? 0xffff0000u : 0u);
         }
         // the PV product; with 8-bit caches (ALU-bound) the token masks are applied only to
         // a unit with fewer than 16 valid rows (a lambda instantiated with and without them)
@@ -1367,7 +1469,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
           }
         };
         if constexpr (KV8) {
-          if (valid < kUnit) pv(std::true_type{});
+          if (!whole) pv(std::true_type{});
           else pv(std::false_type{});
         } else {
           pv(std::true_type{});

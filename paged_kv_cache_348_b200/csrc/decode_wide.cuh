@@ -190,8 +190,8 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
     pa_decode_wide_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv) {
   using L = WideLayout<D>;
-  static_assert(MODE == kPlain || MODE == kPrefix || MODE == kAppend,
-                "wide decode: plain (multi-token), prefix or fused append");
+  static_assert(MODE == kPlain || MODE == kPrefix || MODE == kAppend || MODE == kWindow,
+                "wide decode: plain (multi-token), prefix, fused append or window");
   static_assert(NC == 16 || NC == 32 || NC == 64, "16, 32 or 64 query columns");
   constexpr int kWideSoftThreads = wide_soft_threads(NC);
   constexpr int CW = NC / wide_swg(NC);             // columns of one softmax warpgroup
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
       const int s = base + lane;
       SeqSpan sp{0, 0};
       if (s < B) sp = span_of<MODE>(a, s, c == 0 && kw ? a.status : nullptr);
-      const int u = (sp.ctx + kUnit - 1) / kUnit;
+      const int u = seq_units<MODE>(a, sp.ctx, 0);
       int x = u ? u + kSegW : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
           SeqSpan sp{0, 0};
           if (s < B) sp = span_of<MODE>(a, s, nullptr);
           ctx = sp.ctx;
-          u = (ctx + kUnit - 1) / kUnit;
+          u = seq_units<MODE>(a, ctx, 0);
           x = u ? u + kSegW : 0;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
           pbase += (long long)Hkv * (u_cur ? u_cur + kSegW : 0);
           ++s_cur;
           ctx_cur = span_of<MODE>(a, s_cur, nullptr).ctx;
-          u_cur = (ctx_cur + kUnit - 1) / kUnit;
+          u_cur = seq_units<MODE>(a, ctx_cur, 0);
         }
         const int w_cur = u_cur + kSegW;
         const int kvh = (int)((x - pbase) / w_cur);
@@ -398,6 +398,10 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
         const long long trow_seq = MODE == kPrefix ? (long long)chunk_member(a, s_cur, 0) : s_cur;
         const int32_t* trow = a.block_tables + trow_seq * a.max_blocks;
         const int nblk = (ctx_cur + BS - 1) / BS;
+        // kWindow: scheduled tokens are virtual ones (see WinSpan), else positions
+        [[maybe_unused]] WinSpan win{};
+        if constexpr (MODE == kWindow) win = win_span(a, ctx_cur);
+        const int vctx = MODE == kWindow ? win.vctx() : ctx_cur;
         // block_size 1: the table entries of the portion's next stage, loaded while this
         // stage waits for its slot (pv_tok = the token they start at, -1: none loaded)
         int pv[4] = {-1, -1, -1, -1}, pv_tok = -1;
@@ -446,9 +450,10 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
             for (int rp = 0; rp < kRep; ++rp) {
               const int bi = lane + 32 * rp;
               const int jb = bi;
-              const int t = tok0 + (jb / BPU) * kUnit + (jb % BPU) * H;
+              const int tv = tok0 + (jb / BPU) * kUnit + (jb % BPU) * H;
+              const int t = MODE == kWindow ? win.pos(tv) : tv;
               ys[rp] = -1;
-              if (bi < nbox && t < ctx_cur) {
+              if (bi < nbox && (MODE == kWindow ? win.any_seen(t, H) : t < ctx_cur)) {
                 const int blk = t / BS < nblk ? __ldg(trow + t / BS) : -1;
                 if ((unsigned)blk < (unsigned)a.num_blocks) {
                   ys[rp] = (blk * Hkv + kvh) * BS + (t % BS);
@@ -459,7 +464,11 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
               }
             }
             uint32_t bytes = 0;
-            for (int jj = 0; jj < nun; ++jj) {
+            if constexpr (MODE == kWindow) {
+#pragma unroll
+              for (int rp = 0; rp < kRep; ++rp)
+                bytes += (uint32_t)(__popc(__ballot_sync(0xffffffffu, ys[rp] >= 0)) * kBoxBytes * 2);
+            } else for (int jj = 0; jj < nun; ++jj) {
               const int rem = ctx_cur - (tok0 + jj * kUnit);
               const int nb = (rem + H - 1) / H;
               bytes += (uint32_t)((nb < BPU ? nb : BPU) * kBoxBytes * 2);
@@ -493,19 +502,31 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
             // follows the shared-memory address).  Lane l holds the table entries of rows
             // l, 32+l, 64+l, 96+l, read during the previous stage of the portion (for its
             // first stage: before the slot wait).
-            const int nvalid = (nun * kUnit < ctx_cur - tok0) ? nun * kUnit : ctx_cur - tok0;
+            const int nvalid = (nun * kUnit < vctx - tok0) ? nun * kUnit : vctx - tok0;
+            // the table entry of scheduled token v; kWindow: kUnseen for one that nothing sees
+            constexpr int kUnseen = -2;
+            auto entry = [&](int v) {
+              if constexpr (MODE == kWindow) {
+                const int t = win.pos(v);
+                if (!win.seen(t)) return kUnseen;
+                const int b = __ldg(trow + t);
+                return b < 0 ? -1 : b;
+              } else {
+                return __ldg(trow + v);
+              }
+            };
             int wv[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int r = j * 32 + lane;
-              wv[j] = pv_tok == tok0 ? pv[j] : (r < nvalid ? __ldg(trow + tok0 + r) : -1);
+              wv[j] = pv_tok == tok0 ? pv[j] : (r < nvalid ? entry(tok0 + r) : -1);
             }
             if (tu + kWideUnits < pe) {                // warp-uniform: the next stage's entries
               const int t1 = tok0 + kWideTile;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const int r = j * 32 + lane;
-                pv[j] = t1 + r < ctx_cur ? __ldg(trow + t1 + r) : -1;
+                pv[j] = t1 + r < vctx ? entry(t1 + r) : -1;
               }
               pv_tok = t1;
             }
@@ -540,7 +561,7 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
                 if (i < nitems && r < nvalid) {
                   if ((unsigned)blk < (unsigned)a.num_blocks) {
                     y[q4] = blk * Hkv + kvh;
-                  } else if (a.status && hf == 0 && kv == 0) {
+                  } else if (a.status && hf == 0 && kv == 0 && (MODE != kWindow || blk != kUnseen)) {
                     atomicOr(a.status, DEV_BAD_BLOCK_ID);
                   }
                 }
@@ -771,16 +792,31 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
       tld((uint32_t)(st * 64 + c0), s);
       tmem_wait_ld();
       const int nvalid = (mt.nunits * kUnit < mt.ctx - mt.tok0) ? mt.nunits * kUnit : mt.ctx - mt.tok0;
-      const bool tv = r < nvalid;
+      bool tv = r < nvalid;
       // causal limit: new token j sees stage rows < lim0 + j (a prefix launch: no mask)
-      const int lim0 = MODE == kPrefix ? (1 << 30) : mt.ctx - a.q_len + 1 - mt.tok0;
+      int lim0 = MODE == kPrefix ? (1 << 30) : mt.ctx - a.q_len + 1 - mt.tok0;
+      // kWindow: this row's position decides; new token j sees it when r < lim0 + j and
+      // (j < wend or it is one of the first tokens), wend = its distance from the end of
+      // new token 0's window, so every token sees it when wend >= q_len
+      [[maybe_unused]] int wend = 1 << 30;
+      if constexpr (MODE == kWindow) {
+        const WinSpan win = win_span(a, mt.ctx);
+        const int t = win.pos(mt.tok0 + r);
+        tv = r < mt.nunits * kUnit && win.seen(t);
+        lim0 = mt.ctx - a.q_len + 1 - t + r;
+        if (t >= a.num_sinks) {
+          const long long d = (long long)t + a.window - (mt.ctx - a.q_len);
+          wend = d < (1 << 30) ? (int)d : 1 << 30;
+        }
+      }
       // reference maxima in force: a portion's first stage starts from the -inf row.  With
       // x = scale * s (base 2), e = max_j (x_j - m_j) tells whether a reference must move;
       // masked scores are -inf (NaN against a -inf reference, which fmaxf ignores)
       const float sc = a.scale_log2;
       const float* mcur = mref + (first ? 2 : cur) * kWideCols;
       float e = -INFINITY;
-      if (tv && (MODE == kPrefix || r < lim0)) {   // every column sees this row
+      if (tv && (MODE == kPrefix || r < lim0) && (MODE != kWindow || wend >= a.q_len)) {
+        // every column sees this row
         if (a.ncol < c0 + CW) {                    // padding columns of this warpgroup
 #pragma unroll
           for (int j = 0; j < CW; ++j)
@@ -798,7 +834,8 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
 #pragma unroll
         for (int j = 0; j < CW; ++j) {
           const int cq = c0 + j;
-          const bool vis = tv && cq < a.ncol && (MODE == kPrefix || r < lim0 + colj[cq]);
+          const bool vis = tv && cq < a.ncol && (MODE == kPrefix || r < lim0 + colj[cq]) &&
+                           (MODE != kWindow || colj[cq] < wend);
           if (!vis) s[j] = -INFINITY;
           e = fmaxf(e, fmaf(s[j], sc, -mcur[cq]));
         }

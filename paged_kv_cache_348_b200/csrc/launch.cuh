@@ -125,10 +125,12 @@ PKV_DECL_RUN(pkv::kPlain, false)
 PKV_DECL_RUN(pkv::kPrefix, false)
 PKV_DECL_RUN(pkv::kSuffix, false)
 PKV_DECL_RUN(pkv::kAppend, false)
+PKV_DECL_RUN(pkv::kWindow, false)
 PKV_DECL_RUN(pkv::kPlain, true)
 PKV_DECL_RUN(pkv::kPrefix, true)
 PKV_DECL_RUN(pkv::kSuffix, true)
 PKV_DECL_RUN(pkv::kAppend, true)
+PKV_DECL_RUN(pkv::kWindow, true)
 #undef PKV_DECL_RUN
 
 // ---- the tcgen05 kernel for 9..64 query rows per kv head (decode_wide.cuh); NC = the
@@ -186,6 +188,9 @@ PKV_DECL_WIDE(pkv::kPrefix, 64)
 PKV_DECL_WIDE(pkv::kAppend, 16)
 PKV_DECL_WIDE(pkv::kAppend, 32)
 PKV_DECL_WIDE(pkv::kAppend, 64)
+PKV_DECL_WIDE(pkv::kWindow, 16)
+PKV_DECL_WIDE(pkv::kWindow, 32)
+PKV_DECL_WIDE(pkv::kWindow, 64)
 #undef PKV_DECL_WIDE
 
 }  // namespace pkv_host

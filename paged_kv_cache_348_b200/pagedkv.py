@@ -19,8 +19,8 @@ LIB_PATH = os.path.join(_HERE, "libpagedkv.so")
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_NO_BLOCKS, PA_ERR_NO_MEMORY = \
     0, 1, 2, 3, 4, 5
 PA_F16, PA_BF16 = 0, 1
-DEV_BAD_BLOCK_ID, DEV_BAD_SLOT, DEV_BAD_PAIR, DEV_BAD_CONTEXT_LEN, DEV_TIMEOUT = (
-    0x1, 0x2, 0x4, 0x8, 0x10)
+DEV_BAD_BLOCK_ID, DEV_BAD_SLOT, DEV_BAD_PAIR, DEV_BAD_CONTEXT_LEN, DEV_TIMEOUT, DEV_BAD_KEEP = (
+    0x1, 0x2, 0x4, 0x8, 0x10, 0x20)
 
 # every symbol include/pagedkv.h declares
 EXPORTS = ("pa_version", "pa_status_string", "pa_decode_workspace_bytes", "pa_decode",
@@ -34,7 +34,8 @@ EXPORTS = ("pa_version", "pa_status_string", "pa_decode_workspace_bytes", "pa_de
            "pa_bm_slot_of", "pa_bm_plan_cascade", "pa_plan_cascade", "pa_bm_swap_out",
            "pa_bm_swap_in", "pa_swap_out_blocks", "pa_swap_in_blocks", "pa_cache_append_e4m3_bs",
            "pa_decode_e4m3_bs", "pa_decode_cascade_e4m3_bs", "pa_decode_append_e4m3_bs",
-           "pa_check_bounded_waits")
+           "pa_check_bounded_waits", "pa_decode_window", "pa_decode_window_e4m3_bs",
+           "pa_compact_tokens", "pa_compact_tokens_e4m3_bs")
 
 _lib = None
 _lock = threading.Lock()
@@ -69,6 +70,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                       f32, i32, P, sz, P, P]
         L.pa_check_bounded_waits.restype = i32
         L.pa_check_bounded_waits.argtypes = [P, i32, P]
+        L.pa_decode_window.restype = i32
+        L.pa_decode_window.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32,
+                                       i32, i32, f32, i32, P, sz, P, P]
+        L.pa_decode_window_e4m3_bs.restype = i32
+        L.pa_decode_window_e4m3_bs.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32,
+                                               i32, i32, i32, i32, i32, f32, i32, P, sz, P, P]
+        L.pa_compact_tokens.restype = i32
+        L.pa_compact_tokens.argtypes = [P, P, i32, P, i32, P, i32, P, P, P, i32, i32, i32, i32,
+                                        i32, i32, i32, i32, i32, P, P]
+        L.pa_compact_tokens_e4m3_bs.restype = i32
+        L.pa_compact_tokens_e4m3_bs.argtypes = [P, P, P, P, i32, P, i32, P, i32, P, P, P, i32,
+                                                i32, i32, i32, i32, i32, i32, i32, P, P]
         L.pa_decode_append.restype = i32
         L.pa_decode_append.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32,
                                        f32, i32, P, sz, P, P]
@@ -459,6 +472,85 @@ def pa_decode_append_e4m3_bs(out, q, k_cache8, v_cache8, k_scales, v_scales, k_n
     return out
 
 
+def _here(what, *tensors):
+    """The calls run on the current device: tensors of another one are refused."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise PagedKVError("%s: tensors on %s, the current device is cuda:%d"
+                               % (what, t.device, dev))
+
+
+def _whole(x, name: str) -> int:
+    """A whole number as the C int it becomes, saturated at the largest one."""
+    if not isinstance(x, int):
+        raise PagedKVError("%s must be an int" % name)
+    return max(-1, min(x, 0x7fffffff))
+
+
+def _window_shapes(what, out, q, k_cache, v_cache, block_tables, context_lens, workspace):
+    """Shared checks of the windowed decode calls; (B, QL, Hq, D, N, Hkv, bs)."""
+    if q.dim() not in (3, 4):
+        raise PagedKVError("q must have 3 or 4 dims")
+    _need(q, "q")
+    _need(out, "out", dtype=q.dtype, ndim=q.dim())
+    _need(block_tables, "block_tables", dtype=torch.int32, ndim=2)
+    _need(context_lens, "context_lens", dtype=torch.int32, ndim=1)
+    _need(workspace, "workspace")
+    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
+    N, Hkv, bs, D2 = k_cache.shape
+    if out.shape != q.shape or D2 != D or v_cache.shape != k_cache.shape or \
+            block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise PagedKVError("%s: inconsistent shapes" % what)
+    return B, q.shape[1] if q.dim() == 4 else 1, Hq, D, N, Hkv, bs
+
+
+def pa_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, window: int,
+                     num_sinks: int, scale: float, workspace, status=None, stream=None):
+    """out <- paged decode with a sliding window of `window` positions and `num_sinks` first
+    tokens that stay visible; q and out [B,Hq,D] (one new token) or [B,QL,Hq,D] (QL new
+    tokens, causal).  Table entries of pages that no new token sees are not read (see
+    pa_decode_window in include/pagedkv.h)."""
+    _need(k_cache, "k_cache", dtype=q.dtype, ndim=4)
+    _need(v_cache, "v_cache", dtype=q.dtype, ndim=4)
+    B, QL, Hq, D, N, Hkv, bs = _window_shapes("pa_decode_window", out, q, k_cache, v_cache,
+                                              block_tables, context_lens, workspace)
+    _here("pa_decode_window", out, q, k_cache, v_cache, block_tables, context_lens, workspace,
+          status)
+    rc = load().pa_decode_window(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
+        B, QL, Hq, Hkv, D, bs, block_tables.shape[1], N, _whole(window, "window"),
+        _whole(num_sinks, "num_sinks"), float(scale), _dtype_code(q), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+    _check(rc, "pa_decode_window")
+    return out
+
+
+def pa_decode_window_e4m3_bs(out, q, k_cache8, v_cache8, k_scales, v_scales, block_tables,
+                             context_lens, window: int, num_sinks: int, scale: float, workspace,
+                             status=None, stream=None):
+    """pa_decode_window over uint8 E4M3 pools with per-(block, kv head) scales (see
+    pa_decode_window_e4m3_bs in include/pagedkv.h)."""
+    _need(k_cache8, "k_cache", dtype=torch.uint8, ndim=4)
+    _need(v_cache8, "v_cache", dtype=torch.uint8, ndim=4)
+    _need(k_scales, "k_scales", dtype=torch.float32, ndim=2)
+    _need(v_scales, "v_scales", dtype=torch.float32, ndim=2)
+    B, QL, Hq, D, N, Hkv, bs = _window_shapes("pa_decode_window_e4m3_bs", out, q, k_cache8,
+                                              v_cache8, block_tables, context_lens, workspace)
+    if k_scales.shape != (N, Hkv) or v_scales.shape != (N, Hkv):
+        raise PagedKVError("pa_decode_window_e4m3_bs: inconsistent shapes")
+    _here("pa_decode_window_e4m3_bs", out, q, k_cache8, v_cache8, k_scales, v_scales,
+          block_tables, context_lens, workspace, status)
+    rc = load().pa_decode_window_e4m3_bs(
+        _ptr(out), _ptr(q), _ptr(k_cache8), _ptr(v_cache8), _ptr(k_scales), _ptr(v_scales),
+        _ptr(block_tables), _ptr(context_lens), B, QL, Hq, Hkv, D, bs, block_tables.shape[1], N,
+        _whole(window, "window"), _whole(num_sinks, "num_sinks"), float(scale), _dtype_code(q),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+        _stream(stream))
+    _check(rc, "pa_decode_window_e4m3_bs")
+    return out
+
+
 def pa_cache_append(k_cache, v_cache, k, v, slot_mapping, status=None, stream=None):
     """Scatter k/v [T,Hkv,D] into the pools at slot_mapping (int64 [T])."""
     _need(k_cache, "k_cache", ndim=4)
@@ -541,6 +633,66 @@ def pa_swap_in_blocks(k_caches, v_caches, blocks, buf, status=None, stream=None)
     rc = load().pa_swap_in_blocks(kp, vp, L, _ptr(blocks), n, N, _ptr(buf), bb, _ptr(status),
                                   _stream(stream))
     _check(rc, "pa_swap_in_blocks")
+
+
+def _compact_args(what, k_caches, v_caches, src_tables, dst_tables, context_lens, keep,
+                  keep_lens, status):
+    """Shared checks of the compaction calls, and the arguments from src_tables on."""
+    L, kp, vp, N, _ = _pool_args(k_caches, v_caches)
+    _, Hkv, bs, D = k_caches[0].shape
+    _need(src_tables, "src_tables", dtype=torch.int32, ndim=2)
+    _need(dst_tables, "dst_tables", dtype=torch.int32, ndim=2)
+    _need(context_lens, "context_lens", dtype=torch.int32, ndim=1)
+    _need(keep, "keep", dtype=torch.int32, ndim=4)
+    _need(keep_lens, "keep_lens", dtype=torch.int32, ndim=1)
+    B = src_tables.shape[0]
+    KL, KB, KH, kmax = keep.shape
+    if dst_tables.shape[0] != B or context_lens.shape[0] != B or keep_lens.shape[0] != B or \
+            KB != B or KL not in (1, L) or KH not in (1, Hkv):
+        raise PagedKVError("%s: inconsistent shapes" % what)
+    _here(what, *k_caches, *v_caches, src_tables, dst_tables, context_lens, keep, keep_lens,
+          status)
+    args = [_ptr(src_tables), src_tables.shape[1], _ptr(dst_tables), dst_tables.shape[1],
+            _ptr(context_lens), _ptr(keep), _ptr(keep_lens), kmax, int(KL > 1), int(KH > 1), B,
+            Hkv, D]
+    return L, kp, vp, args, bs, N
+
+
+def pa_compact_tokens(k_caches, v_caches, src_tables, dst_tables, context_lens, keep, keep_lens,
+                      status=None, stream=None):
+    """Move the kept tokens of each sequence (int32 keep[L or 1, B, Hkv or 1, max_keep],
+    ascending positions, keep_lens[B] of them) to positions 0, 1, ... of dst_tables in every
+    layer's K and V pool (lists of 16-bit pools, or of uint8 pools with one scale per pool);
+    see pa_compact_tokens in include/pagedkv.h."""
+    L, kp, vp, args, bs, N = _compact_args("pa_compact_tokens", k_caches, v_caches, src_tables,
+                                           dst_tables, context_lens, keep, keep_lens, status)
+    rc = load().pa_compact_tokens(kp, vp, L, *args, k_caches[0].element_size(), bs, N,
+                                  _ptr(status), _stream(stream))
+    _check(rc, "pa_compact_tokens")
+
+
+def pa_compact_tokens_e4m3_bs(k_caches, v_caches, k_scales, v_scales, src_tables, dst_tables,
+                              context_lens, keep, keep_lens, status=None, stream=None):
+    """pa_compact_tokens over uint8 E4M3 pools with per-(block, kv head) scales (lists of
+    float32 [N, Hkv], one a layer): the kept rows are quantised with their new block's scale,
+    which its first row fixes; see pa_compact_tokens_e4m3_bs in include/pagedkv.h."""
+    L, kp, vp, args, bs, N = _compact_args("pa_compact_tokens_e4m3_bs", k_caches, v_caches,
+                                           src_tables, dst_tables, context_lens, keep, keep_lens,
+                                           status)
+    if k_caches[0].dtype != torch.uint8:
+        raise PagedKVError("pa_compact_tokens_e4m3_bs: pools must be torch.uint8")
+    if len(k_scales) != L or len(v_scales) != L:
+        raise PagedKVError("pa_compact_tokens_e4m3_bs: one scale array per pool")
+    for t in (*k_scales, *v_scales):
+        _need(t, "scales", dtype=torch.float32, ndim=2)
+        if t.shape != k_caches[0].shape[:2]:
+            raise PagedKVError("pa_compact_tokens_e4m3_bs: inconsistent shapes")
+    _here("pa_compact_tokens_e4m3_bs", *k_scales, *v_scales)
+    ks = (ctypes.c_void_p * L)(*[t.data_ptr() for t in k_scales])
+    vs = (ctypes.c_void_p * L)(*[t.data_ptr() for t in v_scales])
+    rc = load().pa_compact_tokens_e4m3_bs(kp, vp, ks, vs, L, *args, bs, N, _ptr(status),
+                                          _stream(stream))
+    _check(rc, "pa_compact_tokens_e4m3_bs")
 
 
 NOALLOC_MAX_SEQS = 16384
