@@ -71,6 +71,7 @@ typedef enum { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
 #define PA_DEV_BAD_PAIR 0x4
 #define PA_DEV_BAD_CONTEXT_LEN 0x8
 #define PA_DEV_BAD_KEEP 0x20 /* a kept position or count out of range (pa_compact_tokens) */
+#define PA_DEV_BAD_QUERY 0x40 /* q_starts not ascending within [0, total_q] (pa_prefill_window) */
 #define PA_DEV_TIMEOUT 0x10 /* a pipeline wait gave up after ~2 s; outputs are invalid */
 
 /* Library ABI version (major*100 + minor). */
@@ -184,6 +185,37 @@ pa_status pa_decode_window_e4m3_bs(void* out, const void* q, const void* k_cache
                                    int max_blocks_per_seq, int num_blocks, int window,
                                    int num_sinks, float scale, pa_dtype dtype, void* workspace,
                                    size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * pa_prefill_window -- the attention of pa_decode_window for prompt chunks: any number of new
+ * tokens per sequence, a different one for each.
+ *
+ * Defined by the passages of pa_decode and pa_decode_multi.  The new tokens of sequence s are
+ * the n = q_starts[s + 1] - q_starts[s] rows of q from q_starts[s] on, its last n cached
+ * positions (append them first): token i sits at p = context_lens[s] - n + i and sees
+ *   { t : 0 <= t <= p and (t > p - window or t < num_sinks) };
+ * a window of context_lens[s] or more is the plain causal mask.  A token with p < 0 sees
+ * nothing: its row is zero.  What lies outside every window may hold anything, as for
+ * pa_decode_window; the rows that some new token of a sequence sees must be finite for all
+ * of its tokens.
+ *
+ *   q, out         [total_q][num_q_heads][head_dim]; rows of no sequence are not written
+ *   q_starts       device int32 [num_seqs + 1], ascending (equal: no new tokens), in
+ *                  [0, total_q]; a sequence whose pair is out of range counts as empty and
+ *                  sets PA_DEV_BAD_QUERY
+ *   workspace      >= pa_prefill_workspace_bytes() bytes, 16-byte aligned; its contents on
+ *                  entry do not matter.  Calls that may run at the same time need one each.
+ *   other arguments and errors as for pa_decode (16-bit pools; any number of q heads per kv
+ *   head).  Weights are rounded to the cache's type before they meet V.
+ */
+size_t pa_prefill_workspace_bytes(void);
+pa_status pa_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_tables, const int32_t* context_lens,
+                            const int32_t* q_starts, int total_q, int num_seqs, int num_q_heads,
+                            int num_kv_heads, int head_dim, int block_size,
+                            int max_blocks_per_seq, int num_blocks, int window, int num_sinks,
+                            float scale, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                            int32_t* dev_status, void* stream);
 
 /*
  * pa_decode_append -- pa_cache_append of each sequence's newest token fused into

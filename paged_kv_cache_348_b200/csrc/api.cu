@@ -291,6 +291,9 @@ pa_status decode_impl(void* out, const void* q, const void* k_cache, const void*
   a.q_len = q_len;
   a.ncol = group * q_len;
   a.scale_log2 = scale * cx.k_scale * 1.4426950408889634f;
+  // the tcgen05 kernel scales after masking: 0 * -inf would be NaN, and 1e-37 gives the same
+  // weights (all 1)
+  if (wide && a.scale_log2 == 0.f) a.scale_log2 = 1e-37f;
   a.v_scale = cx.v_scale;
   a.epoch = next_epoch();
   a.seq_start = cx.seq_start;
@@ -475,6 +478,81 @@ pa_status pa_decode_window_e4m3_bs(void* out, const void* q, const void* k_cache
                      num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
                      num_blocks, scale, dtype, workspace, workspace_bytes, 0, dev_status, stream,
                      cx);
+}
+
+size_t pa_prefill_workspace_bytes(void) { return 256; }
+
+pa_status pa_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_tables, const int32_t* context_lens,
+                            const int32_t* q_starts, int total_q, int num_seqs, int num_q_heads,
+                            int num_kv_heads, int head_dim, int block_size,
+                            int max_blocks_per_seq, int num_blocks, int window, int num_sinks,
+                            float scale, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                            int32_t* dev_status, void* stream) {
+  if (total_q < 0 || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      max_blocks_per_seq <= 0 || num_blocks <= 0 || !std::isfinite(scale) || window < 1 ||
+      num_sinks < 0)
+    return PA_ERR_INVALID;
+  if (num_q_heads % num_kv_heads) return PA_ERR_INVALID;
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (block_size != 1 && block_size != 8 && block_size != 16 && block_size != 32)
+    return PA_ERR_UNSUPPORTED;
+  // query rows of a sequence, cached positions and pool rows are counted in 32 bits
+  if ((long long)total_q * num_q_heads >= (1ll << 31) - 512 ||
+      (long long)num_blocks * num_kv_heads * block_size >= (1ll << 31) ||
+      (long long)max_blocks_per_seq * block_size >= (1ll << 31) - 512)
+    return PA_ERR_INVALID;
+  if (num_seqs == 0 || total_q == 0) return PA_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !q_starts ||
+      !workspace)
+    return PA_ERR_INVALID;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(workspace) || workspace_bytes < pa_prefill_workspace_bytes())
+    return PA_ERR_INVALID;
+  const int sms = sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
+  CUtensorMap mk, mv;
+  std::memset(&mk, 0, sizeof(mk));
+  std::memset(&mv, 0, sizeof(mv));
+  const uint64_t rows = (uint64_t)num_blocks * num_kv_heads * block_size;
+  const int groups = block_size < 16 ? 1 : 2;      // 8-row groups of a box
+  if (block_size == 1 ? !encode_pool(&mk, k_cache, dtype, head_dim, rows, 1) ||
+                            !encode_pool(&mv, v_cache, dtype, head_dim, rows, 1)
+                      : !encode_pool_wide(&mk, k_cache, dtype, head_dim, rows, groups) ||
+                            !encode_pool_wide(&mv, v_cache, dtype, head_dim, rows, groups))
+    return PA_ERR_CUDA;
+  pkv::PrefillArgs a{};
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.q_starts = q_starts;
+  a.status = dev_status;
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = num_q_heads / num_kv_heads;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.ctx_cap = max_blocks_per_seq * block_size;
+  a.window = std::min(window, a.ctx_cap);
+  a.num_sinks = std::min(num_sinks, a.ctx_cap);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  // at most one row tile per 256 query rows and one more per sequence, for every kv head
+  const long long most = ((long long)total_q * a.group / pkv::kPfRows + num_seqs) * num_kv_heads;
+  const int grid = (int)std::min<long long>(sms, most);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (most > sms) {                                // CTAs draw items past their first
+    a.ticket = static_cast<unsigned long long*>(workspace);
+    if (cudaMemsetAsync(a.ticket, 0, sizeof(*a.ticket), st) != cudaSuccess) return PA_ERR_CUDA;
+  }
+  return dtype == PA_BF16
+             ? pkv_host::run_prefill_bf16(head_dim, block_size, a, mk, mv, grid, st)
+             : pkv_host::run_prefill_f16(head_dim, block_size, a, mk, mv, grid, st);
 }
 
 pa_status pa_decode_append(void* out, const void* q, void* k_cache, void* v_cache,

@@ -1,0 +1,706 @@
+// prefill.cuh -- attention of ragged prompt chunks over a paged cache, with a sliding window
+// and a few first tokens that stay visible, on the tcgen05 tensor cores.
+//
+// The operation is the one of decode.cuh ("Paged Attention and Memory Efficiency in
+// Production LLM Serving", section "How PagedAttention borrows OS paging": the kernel
+// resolves the block table, the arithmetic is the plain softmax(scale q K^T) V) for
+// sequences with many new tokens: token i of n at position p = ctx - n + i sees the cached
+// positions t <= p with t > p - window or t < num_sinks.
+//
+// What bounds it: with n new tokens every K/V row is used by up to n * group query rows, so
+// past a few hundred rows it is the contractions (4 D flop per query row and visible
+// position) and, next to them, one exponential per score: a 128 x 128 tile of scores costs
+// the tensor cores 2 x 512 cycles at D = 128 and the special-function units (16 a cycle and
+// SM) 1024, so the two have to run side by side.
+//
+//  * An item is 256 query rows (token-major: row = token * group + head of the group, so the
+//    heads of a kv head share every K/V byte) of one (sequence, kv head), as two subtiles of
+//    128 rows.  While the softmax of one subtile runs, the tensor cores work on the other.
+//  * Key tiles are 128 positions.  As in decode.cuh the first tokens are laid directly in
+//    front of the window ("virtual" positions, rounded to 32), so a tile of a few first
+//    tokens is not paid for on its own; positions between are neither loaded nor computed.
+//  * Tensor memory, 512 columns: S of either subtile (128 columns each) and O of either.
+//    P goes over the S it came from, 16 bits a value, and is the A operand of P V from
+//    there.  Tensor-core operations of one thread execute in order, so Q K^T of the next key
+//    tile may overwrite P right behind the P V that reads it.
+//  * Softmax: one thread per query row, base 2 in 32 bits, so a row's maximum and sum need
+//    no exchange.  The reference maximum moves only when a score passes it by 2^8 (O is
+//    then rescaled in tensor memory); after a row's first key tile that is rare.  The row
+//    sum takes the weights before they are rounded to 16 bits.  A weight rounded to the
+//    cache's type (bf16: half a step 2^-9..2^-8) is off by as much as the output's own
+//    rounding; carrying its residual too, as decode does, would make P V half as fast in a
+//    kernel that the tensor cores bound.
+//  * Warps 0-3 and 4-7: softmax and output of the two subtiles; 8: one thread issues the
+//    tensor-core operations; 9: K and V tiles by TMA through the block table into a ring of
+//    tiles; 10: query rows; 11: hands out items.  Items go to CTAs as they become free (one
+//    CTA an SM), since a causal prompt's items differ in length.
+//  * Rows of V that no query of the sequence sees may hold anything (NaN times a weight of 0
+//    would reach O): units that hold such rows are copied row by row with zeros in their
+//    place, everything else comes by TMA boxes.  Scores are masked by selection.
+//  * Every wait is bounded; tensor memory is released on every path.
+#pragma once
+#include <climits>
+
+#include "decode_wide.cuh"
+
+namespace pkv {
+
+constexpr int DEV_BAD_QUERY = 0x40;
+constexpr int kPfSub = 128;                       // query rows of a subtile (MMA M)
+constexpr int kPfRows = 2 * kPfSub;               // query rows of an item
+constexpr int kPfKeys = 128;                      // positions of a key tile
+constexpr int kPfThreads = 384;
+constexpr int kPfItems = 2;                       // items a CTA has in flight
+constexpr int kPfAlign = 32;                      // granularity of the virtual positions
+
+struct PrefillArgs {
+  void* out;
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* q_starts;                        // [num_seqs + 1] first query row (token) each
+  unsigned long long* ticket;                     // items drawn; null: one item a CTA at most
+  int32_t* status;
+  int num_seqs, total_q, num_q_heads, num_kv_heads, group, max_blocks, num_blocks, ctx_cap;
+  int window, num_sinks;
+  float scale_log2;
+};
+
+// One item, as handed to the warps of its CTA.
+struct PfItem {
+  int seq, kvh;
+  int q0;                                         // first token row of the sequence in q, out
+  int row0, rows;                                 // query rows row0 .. of the sequence
+  int pos0;                                       // position of the sequence's first new token
+  int ctx, w0;                                    // length; first position its queries' windows reach
+  int lo, last;                                   // the item's first window position, last position
+  int head, jump;                                 // virtual position v is v (< head) or v + jump
+  int tiles;                                      // key tiles; 0: nothing visible
+  int end;                                        // no more items
+};
+
+template <int D>
+struct PfLayout {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kGroupBytes = kHalves * 1024;           // 8 rows, all halves
+  static constexpr int kTileBytes = kHalves * kPfKeys * 128;   // one K or V tile
+  static constexpr int kSubBytes = kHalves * kPfSub * 128;     // one subtile of Q
+  static constexpr int kSlots = D == 128 ? 5 : 8;              // K and V tiles in flight
+  static constexpr int kQOff = kSlots * kTileBytes;
+  static constexpr int kItemOff = kQOff + 2 * kSubBytes;
+  static constexpr int kBarOff = (kItemOff + kPfItems * (int)sizeof(PfItem) + 15) / 16 * 16;
+  // kvfull, kvempty [slots]; itemfull, itemempty [items]; sfull, pfull, odone [2]; qfull, qempty,
+  // loaded, drain
+  static constexpr int kNumBars = 2 * kSlots + 2 * kPfItems + 6 + 4;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;      // tmem base, abort flag
+  static constexpr int kBytes = kMiscOff + 16;
+  static constexpr int kDynSmem = kBytes + 1024;
+  static_assert(kTileBytes % 1024 == 0 && kQOff % 1024 == 0 && kSubBytes % 1024 == 0,
+                "128-byte swizzle atoms need 1024-byte alignment");
+  static_assert(kDynSmem <= 232448, "one CTA per SM must fit");
+};
+
+// Position of virtual position v of an item.
+__device__ __forceinline__ int pf_pos(const PfItem& it, int v) {
+  return v < it.head ? v : v + it.jump;
+}
+
+// bits r < n (n clamped to 0..32)
+__device__ __forceinline__ uint32_t below32(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
+// Hands out the items of a launch in order, whole warps at a time: sequences in batch order,
+// a sequence's row tiles from its last (longest) to its first, the kv heads of a row tile
+// side by side (their CTAs read the same block-table entries).
+struct PfCursor {
+  long long base = 0;            // first item of the 32 sequences from sbase on
+  int sbase = -32;
+  long long incl = 0, sum = 0;   // this lane's inclusive item count, all lanes'
+  int q0 = 0, n = 0, tiles = 0;
+
+  __device__ __forceinline__ void load(const PrefillArgs& a, int lane) {
+    const int s = sbase + lane;
+    q0 = n = tiles = 0;
+    if (s < a.num_seqs) {
+      int b = a.q_starts[s], e = a.q_starts[s + 1];
+      if (b < 0 || e < b || e > a.total_q) {
+        if (a.status) atomicOr(a.status, DEV_BAD_QUERY);
+        b = e = 0;
+      }
+      q0 = b;
+      n = e - b;
+      tiles = (int)(((long long)n * a.group + kPfRows - 1) / kPfRows);
+    }
+    incl = (long long)tiles * a.num_kv_heads;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    sum = __shfl_sync(0xffffffffu, incl, 31);
+  }
+  // item index i (ascending from call to call); every lane of the warp calls it
+  __device__ __forceinline__ PfItem find(const PrefillArgs& a, long long i, int lane) {
+    PfItem it{};
+    while (sbase < 0 || i >= base + sum) {
+      if (sbase >= 0) base += sum;
+      sbase += 32;
+      if (sbase >= a.num_seqs) {
+        it.end = 1;
+        sum = 0;
+        return it;
+      }
+      load(a, lane);
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, i < base + incl)) - 1;
+    const long long first = base + __shfl_sync(0xffffffffu, incl, src) -
+                            (long long)__shfl_sync(0xffffffffu, tiles, src) * a.num_kv_heads;
+    const int nt = __shfl_sync(0xffffffffu, tiles, src);
+    const int nq = __shfl_sync(0xffffffffu, n, src);
+    it.q0 = __shfl_sync(0xffffffffu, q0, src);
+    it.seq = sbase + src;
+    const int j = (int)(i - first);
+    it.kvh = j % a.num_kv_heads;
+    it.row0 = (nt - 1 - j / a.num_kv_heads) * kPfRows;
+    const int all = nq * a.group;
+    it.rows = all - it.row0 < kPfRows ? all - it.row0 : kPfRows;
+    it.ctx = clamp_ctx(a.context_lens[it.seq], a.ctx_cap, a.status);
+    it.pos0 = it.ctx - nq;
+    auto win0 = [&](int p) {
+      const long long x = (long long)p - a.window + 1;
+      return x > 0 ? (int)x : 0;
+    };
+    it.w0 = win0(it.pos0);
+    it.lo = win0(it.pos0 + it.row0 / a.group);
+    it.last = it.pos0 + (it.row0 + it.rows - 1) / a.group;
+    if (it.last >= 0) {
+      const int ws = it.lo / kPfAlign * kPfAlign;
+      const int hs = a.num_sinks < ws ? (a.num_sinks + kPfAlign - 1) / kPfAlign * kPfAlign : ws;
+      it.head = hs < ws ? hs : ws;
+      it.jump = ws - it.head;
+      it.tiles = (it.last + 1 - it.jump + kPfKeys - 1) / kPfKeys;
+    }
+    return it;
+  }
+};
+
+template <typename T, int D, int BS>
+__global__ void __launch_bounds__(kPfThreads, 1)
+    pa_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv) {
+  using L = PfLayout<D>;
+  constexpr uint32_t kAB = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
+  constexpr uint32_t kOCols = 256;                 // O of subtile j from column 256 + 128 j
+  constexpr int kItemUsers = 8 + 1 + 1 + 1;        // warps that read an item
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sQ = smem + L::kQOff;
+  PfItem* items = reinterpret_cast<PfItem*>(smem + L::kItemOff);
+  uint64_t* kvfull = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* kvempty = kvfull + L::kSlots;
+  uint64_t* itemfull = kvempty + L::kSlots;
+  uint64_t* itemempty = itemfull + kPfItems;
+  uint64_t* sfull = itemempty + kPfItems;
+  uint64_t* pfull = sfull + 2;
+  uint64_t* odone = pfull + 2;
+  uint64_t* qfull = odone + 2;
+  uint64_t* qempty = qfull + 1;
+  uint64_t* loaded = qempty + 1;
+  uint64_t* drain = loaded + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(&kvfull[i], 33);                   // expect_tx and 32 cp.async arrivals
+      mbar_init(&kvempty[i], 1);
+    }
+    for (int i = 0; i < kPfItems; ++i) {
+      mbar_init(&itemfull[i], 1);
+      mbar_init(&itemempty[i], kItemUsers);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], kPfSub);
+      mbar_init(&odone[i], 1);
+    }
+    mbar_init(qfull, 32);
+    mbar_init(qempty, 1);
+    mbar_init(loaded, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 32) {
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  const int Hkv = a.num_kv_heads, group = a.group;
+  auto give_up = [&]() {
+    if (lane == 0) {
+      *abort_flag = 1;
+      if (a.status) atomicOr(a.status, DEV_TIMEOUT);
+    }
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait_bounded(bar, parity, abort_flag, kWaitLimitNs);
+  };
+  // item k of this CTA, or false at the end of the launch (or of patience); item_done hands
+  // its slot back
+  auto item_at = [&](int k, PfItem& it) {
+    const int sl = k % kPfItems;
+    if (!wait(&itemfull[sl], (uint32_t)(k / kPfItems) & 1u)) {
+      give_up();
+      return false;
+    }
+    it = items[sl];
+    return it.end == 0;
+  };
+  auto item_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&itemempty[k % kPfItems]);
+  };
+
+  if (warp < 8) {
+    // ============================== softmax and output ==============================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int sub = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;           // row of the subtile = lane of tensor memory
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tbase + lanes + (uint32_t)(sub * 128);
+    const uint32_t tO = tbase + lanes + kOCols + (uint32_t)(sub * 128);
+    // a scale of 0 is taken as 1e-37, which gives the same weights (1) and keeps a masked
+    // score's -inf * scale from being NaN
+    const float sc = fmaxf(fabsf(a.scale_log2), 1e-37f);
+    const bool neg = a.scale_log2 < 0.f;            // the maximum is taken over unscaled scores
+    uint32_t sph = 0, oph = 0;
+    bool ok = true;
+    PfItem it;
+    for (int k = 0; ok && item_at(k, it); ++k) {
+      const int row = it.row0 + sub * kPfSub + r;   // query row of the sequence
+      const bool mine = sub * kPfSub + r < it.rows;
+      const int token = row / group;
+      // a row past the item's takes part with nothing visible
+      const int p = mine ? it.pos0 + token : -1;
+      const bool active = sub * kPfSub < it.rows && it.tiles > 0;
+      float m = -INFINITY, l = 0.f;
+      if (active) {
+        // tiles [full0, full1) are visible whole to every row of the subtile: after the
+        // last row's window start, up to the first row's own position
+        const int r_last = min(it.rows, (sub + 1) * kPfSub) - 1;
+        const int p_first = it.pos0 + (it.row0 + sub * kPfSub) / group;
+        const int p_last = it.pos0 + (it.row0 + r_last) / group;
+        for (int i = 0; i < it.tiles; ++i) {
+          if (!wait(&sfull[sub], sph)) {
+            give_up();
+            ok = false;
+            break;
+          }
+          sph ^= 1u;
+          tc_fence_after();
+          uint32_t s[128];
+          tmem_ld32(tS, s);
+          tmem_ld32(tS + 32, s + 32);
+          tmem_ld32(tS + 64, s + 64);
+          tmem_ld32(tS + 96, s + 96);
+          tmem_wait_ld();
+          if (neg) {
+#pragma unroll
+            for (int j = 0; j < 128; ++j) s[j] ^= 0x80000000u;
+          }
+          const int v0 = i * kPfKeys;
+          const int t0 = pf_pos(it, v0);
+          // whole: one run of positions, none after the first row's own, none before the
+          // last row's window (or all of them first tokens)
+          const bool whole = (v0 >= it.head || v0 + kPfKeys <= it.head || it.jump == 0) &&
+                             t0 + kPfKeys - 1 <= p_first &&
+                             ((long long)t0 > (long long)p_last - a.window ||
+                              t0 + kPfKeys <= a.num_sinks);
+          if (!whole) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int t = pf_pos(it, v0 + 32 * c);
+              const long long w = (long long)p - a.window + 1 - t;
+              const uint32_t see = below32(p + 1 - t) &
+                                   (~below32(w > 32 ? 32 : (w < 0 ? 0 : (int)w)) | below32(a.num_sinks - t));
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(see >> j & 1u)) s[32 * c + j] = 0xff800000u;
+            }
+          }
+          float mx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            mx[c] = __uint_as_float(s[32 * c]);
+#pragma unroll
+            for (int j = 1; j < 32; ++j) mx[c] = fmaxf(mx[c], __uint_as_float(s[32 * c + j]));
+          }
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // the reference moves on a row's first visible tile and past a gap of 2^8
+          const bool move = mt > m && (m == -INFINITY || (mt - m) * sc > kRescaleLog2);
+          if (__any_sync(0xffffffffu, move)) {
+            const float alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2((m - mt) * sc));
+            if (move) {
+              l *= alpha;
+              m = mt;
+            }
+            // O so far is against the old reference (its last P V is done: it was issued
+            // before the Q K^T whose scores have arrived); before the first P V there is none
+            if (i > 0) {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tO + 32 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                tmem_st32(tO + 32 * c, o);
+              }
+            }
+          }
+          const float ms = m == -INFINITY ? 0.f : m * sc;
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float p0 = ex2(fmaf(__uint_as_float(s[64 * c + 2 * j]), sc, -ms));
+              const float p1 = ex2(fmaf(__uint_as_float(s[64 * c + 2 * j + 1]), sc, -ms));
+              ls[j & 1] += p0;
+              ls[2 + (j & 1)] += p1;
+              pk[j] = pack2<T>(p0, p1);
+            }
+            tmem_st32(tS + 32 * c, pk);
+          }
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&pfull[sub]);
+        }
+        if (ok && !wait(&odone[sub], oph)) {
+          give_up();
+          ok = false;
+        }
+        if (!ok) break;
+        oph ^= 1u;
+        tc_fence_after();
+      }
+      // output rows; a row that sees nothing is zero
+      const float inv = 1.f / l;
+      T* orow = static_cast<T*>(a.out) +
+                (((long long)it.q0 + token) * a.num_q_heads + (long long)it.kvh * group +
+                 (row - token * group)) * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (active) {
+          tmem_ld32(tO + 32 * c, o);
+          tmem_wait_ld();
+        }
+        if (mine) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = l == 0.f ? 0u
+                              : pack2<T>(__uint_as_float(o[8 * u + 2 * j]) * inv,
+                                         __uint_as_float(o[8 * u + 2 * j + 1]) * inv);
+            *reinterpret_cast<uint4*>(orow + 32 * c + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();                            // O is read before the next item's P V
+      item_done(k);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
+      // ============================== tensor-core issue ==============================
+      const uint32_t idesc_qk = idesc_f16(kAB, 0u, 0u, kPfSub, kPfKeys);
+      const uint32_t idesc_pv = idesc_f16(kAB, 0u, 1u, kPfSub, (uint32_t)D);
+      const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16u, 1024u);
+      const uint64_t dk0 = smem_desc_sw128(smem_u32(smem), 16u, L::kGroupBytes);
+      const uint64_t dv0 = smem_desc_sw128(smem_u32(smem), 1024u, L::kGroupBytes);
+      auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
+      uint32_t f = 0, qph = 0, pph[2] = {0, 0};     // K/V tiles taken; phases
+      bool ok = true;
+      PfItem it;
+      for (int k = 0; ok && item_at(k, it); ++k) {
+        if (lane == 0 && it.tiles > 0) {
+          const int nsub = it.rows > kPfSub ? 2 : 1;
+          auto tile = [&](uint32_t fill) {          // a K or V tile has landed
+            const bool got = wait(&kvfull[fill % L::kSlots], (fill / L::kSlots) & 1u);
+            fence_proxy_async_smem();               // parts may have come by cp.async
+            tc_fence_after();
+            return got;
+          };
+          auto qk = [&](int j, uint32_t fill) {
+            const uint32_t so = (fill % L::kSlots) * L::kTileBytes;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = (ks & 3) * 32;
+              tc_mma_f16(tbase + (uint32_t)(j * 128),
+                         adv(dq0, j * L::kSubBytes + (ks >> 2) * (kPfSub * 128) + off),
+                         adv(dk0, so + (ks >> 2) * 1024 + off), idesc_qk, ks > 0);
+            }
+            tc_commit(&sfull[j]);
+          };
+          ok = wait(qfull, qph) && tile(f);
+          qph ^= 1u;
+          if (ok) {
+            for (int j = 0; j < nsub; ++j) qk(j, f);
+            tc_commit(&kvempty[f % L::kSlots]);
+            if (it.tiles == 1) tc_commit(qempty);
+          }
+          for (int i = 0; ok && i < it.tiles; ++i) {
+            const uint32_t fv = f + 2 * i + 1, fk = f + 2 * i + 2;
+            const bool more = i + 1 < it.tiles;
+            ok = tile(fv) && (!more || tile(fk));
+            for (int j = 0; ok && j < nsub; ++j) {
+              if (!wait(&pfull[j], pph[j])) {
+                ok = false;
+                break;
+              }
+              pph[j] ^= 1u;
+              tc_fence_after();
+              const uint32_t so = (fv % L::kSlots) * L::kTileBytes;
+#pragma unroll
+              for (int kk = 0; kk < kPfKeys / 16; ++kk)
+                tc_mma_f16_ts(tbase + kOCols + (uint32_t)(j * 128),
+                              tbase + (uint32_t)(j * 128 + kk * 8),
+                              adv(dv0, so + kk * 2 * L::kGroupBytes), idesc_pv, i > 0 || kk > 0);
+              if (!more) tc_commit(&odone[j]);
+              if (j == nsub - 1) tc_commit(&kvempty[fv % L::kSlots]);
+              if (more) {
+                qk(j, fk);
+                if (j == nsub - 1) {
+                  tc_commit(&kvempty[fk % L::kSlots]);
+                  if (i + 2 == it.tiles) tc_commit(qempty);
+                }
+              }
+            }
+          }
+          f += 2 * it.tiles;
+          if (!ok) {
+            *abort_flag = 1;
+            if (a.status) atomicOr(a.status, DEV_TIMEOUT);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        item_done(k);
+      }
+      if (lane == 0) {
+        // nothing issued here may still run when tensor memory is released
+        tc_commit(drain);
+        int no_abort = 0;
+        mbar_wait_bounded(drain, 0u, &no_abort, kWaitLimitNs);
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // ============================== K and V tiles ==============================
+      const uint64_t policy = policy_evict_normal();
+      const int rows_total = a.num_blocks * Hkv * BS;
+      uint32_t f = 0;
+      bool ok = true;
+      PfItem it;
+      for (int k = 0; ok && item_at(k, it); ++k) {
+        const int32_t* trow = a.block_tables + (long long)it.seq * a.max_blocks;
+        const int S = a.num_sinks;
+        // needed by this item; sure: no position of t .. t+n-1 is hidden from every query of
+        // the sequence (hidden rows may hold anything)
+        auto needed = [&](int t, int n) { return t <= it.last && (t + n > it.lo || t < S); };
+        auto sure = [&](int t, int n) { return t + n <= it.ctx && (t >= it.w0 || t + n <= S); };
+        auto seen = [&](int t) { return t < it.ctx && (t >= it.w0 || t < S); };
+        constexpr int H = BS == 1 ? 1 : (BS < 16 ? BS : 16);   // rows of a TMA box
+        constexpr int kBoxes = kPfKeys / H;
+        constexpr int kE = BS == 1 ? 4 : 1;                    // table entries a lane holds
+        static_assert(kBoxes <= 32 * kE, "one box a lane, or four rows");
+        auto entries = [&](int i, int (&e)[kE]) {
+#pragma unroll
+          for (int x = 0; x < kE; ++x) {
+            const int t = pf_pos(it, i * kPfKeys + (x * 32 + lane) * H);
+            e[x] = (x * 32 + lane < kBoxes && needed(t, H)) ? __ldg(trow + t / BS) : -1;
+          }
+        };
+        int cur[kE], nxt[kE];
+        if (it.tiles) entries(0, cur);
+        for (int i = 0; ok && i < it.tiles; ++i) {
+          if (i + 1 < it.tiles) entries(i + 1, nxt);
+          int y[kE];                                // row coordinate of the box (out of range: zeros)
+          [[maybe_unused]] bool patch = false;      // its V rows are copied one by one
+          bool load_k = false;
+#pragma unroll
+          for (int x = 0; x < kE; ++x) {
+            const int t = pf_pos(it, i * kPfKeys + (x * 32 + lane) * H);
+            y[x] = rows_total;
+            if (x * 32 + lane < kBoxes && needed(t, H) && (BS != 1 || seen(t))) {
+              if ((unsigned)cur[x] < (unsigned)a.num_blocks) {
+                y[x] = (cur[x] * Hkv + it.kvh) * BS + t % BS;
+                load_k = true;
+                patch = BS != 1 && !sure(t, H);
+              } else if (a.status) {
+                atomicOr(a.status, DEV_BAD_BLOCK_ID);
+              }
+            }
+          }
+          for (int kv = 0; ok && kv < 2; ++kv) {
+            const int sl = (int)(f % L::kSlots);
+            if (!wait(&kvempty[sl], ((f / L::kSlots) & 1u) ^ 1u)) {
+              give_up();
+              ok = false;
+              break;
+            }
+            ++f;
+            uint8_t* dst = smem + sl * L::kTileBytes;
+            const CUtensorMap* map = kv ? &tmv : &tmk;
+            if constexpr (BS != 1) {
+              constexpr int kBoxBytes = H * 128 * L::kHalves;
+              // K boxes that nothing needs keep what the slot held (their scores are masked);
+              // V boxes become zeros
+              const bool box = lane < kBoxes && (kv ? !patch : load_k);
+              const unsigned n = __popc(__ballot_sync(0xffffffffu, box));
+              if (lane == 0) mbar_arrive_expect_tx(&kvfull[sl], n * kBoxBytes);
+              __syncwarp();
+              if (box)
+                tma_load_4d(dst + lane * (H / 8) * L::kGroupBytes, map, &kvfull[sl], y[0] >> 3,
+                            policy);
+              unsigned todo = kv ? __ballot_sync(0xffffffffu, patch) : 0u;
+              while (todo) {
+                const int b = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const int t = pf_pos(it, i * kPfKeys + b * H);
+                const long long yb = __shfl_sync(0xffffffffu, y[0], b);
+                constexpr int CPR = D / 8;          // 16-byte pieces of a row
+                for (int x = lane; x < H * CPR; x += 32) {
+                  const int rr = x / CPR, ch = x % CPR, tr = b * H + rr;
+                  cp_async_16_zfill(dst + (tr >> 3) * L::kGroupBytes + (ch >> 3) * 1024 +
+                                        (tr & 7) * 128 + (((ch & 7) ^ (tr & 7)) << 4),
+                                    static_cast<const T*>(a.v_cache) + (yb + rr) * D + ch * 8,
+                                    seen(t + rr) ? 16u : 0u);
+                }
+              }
+            } else {
+              // four rows a gather load, one 128-byte half of each
+              if (lane == 0) mbar_arrive_expect_tx(&kvfull[sl], L::kTileBytes);
+              __syncwarp();
+#pragma unroll
+              for (int x = 0; x < L::kHalves; ++x) {
+                const int e = x * 32 + lane, hf = e % L::kHalves, g = e / L::kHalves;
+                int z[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const int rr = 4 * g + u;         // row of the tile
+                  int v[4];
+#pragma unroll
+                  for (int w = 0; w < 4; ++w) v[w] = __shfl_sync(0xffffffffu, y[w], rr & 31);
+                  z[u] = rr < 32 ? v[0] : (rr < 64 ? v[1] : (rr < 96 ? v[2] : v[3]));
+                }
+                tma_gather4(dst + (g >> 1) * L::kGroupBytes + hf * 1024 + (g & 1) * 512, map,
+                            &kvfull[sl], hf * 64, z[0], z[1], z[2], z[3], policy);
+              }
+            }
+            cp_async_mbar_arrive_noinc(&kvfull[sl]);
+          }
+#pragma unroll
+          for (int x = 0; x < kE; ++x) cur[x] = nxt[x];
+        }
+        item_done(k);
+        if (lane == 0) mbar_arrive(loaded);
+      }
+      // copies still in flight (only after a failed wait) land before the CTA's memory goes
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!ok || *abort_flag) {
+        int no_abort = 0;
+        for (uint32_t g = f > L::kSlots ? f - L::kSlots : 0; g < f; ++g)
+          mbar_wait_bounded(&kvfull[g % L::kSlots], (g / L::kSlots) & 1u, &no_abort, kWaitLimitNs);
+      }
+    } else if (warp == 10) {
+      // ============================== query rows ==============================
+      int used = 0;
+      PfItem it;
+      for (int k = 0; item_at(k, it); ++k) {
+        if (it.tiles > 0) {
+          if (used > 0 && !wait(qempty, (uint32_t)(used - 1) & 1u)) {
+            give_up();
+            break;
+          }
+          ++used;
+          constexpr int CPR = D / 8;
+          const T* base = static_cast<const T*>(a.q) + (long long)it.q0 * a.num_q_heads * D +
+                          (long long)it.kvh * group * D;
+          const int rows = it.rows > kPfSub ? kPfRows : kPfSub;
+          constexpr int kStep = 32 / CPR;           // rows the warp covers at a time
+          const int ch = lane % CPR;
+          for (int x = lane / CPR; x < rows; x += kStep) {
+            const bool in = x < it.rows;
+            const int row = it.row0 + (in ? x : 0), token = row / group;
+            const T* src = base + ((long long)token * a.num_q_heads + (row - token * group)) * D;
+            const int xr = x & (kPfSub - 1);
+            cp_async_16_zfill(sQ + (x / kPfSub) * L::kSubBytes + (ch >> 3) * (kPfSub * 128) +
+                                  xr * 128 + (((ch & 7) ^ (xr & 7)) << 4),
+                              src + ch * 8, in ? 16u : 0u);
+          }
+          cp_async_mbar_arrive_noinc(qfull);
+        }
+        item_done(k);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      // ============================== items ==============================
+      // The first item is the CTA's index; the later ones are drawn from a counter shared by
+      // the launch (zeroed before it), one at a time and late: when every tile of the item
+      // before is on its way, so that a CTA does not sit on work while others run dry.
+      PfCursor cur;
+      long long i = blockIdx.x;
+      for (int k = 0;; ++k) {
+        if (k > 0) {
+          // item k - 1 is loaded, and the slot of item k - kPfItems is free
+          if (!wait(loaded, (uint32_t)(k - 1) & 1u) ||
+              (k >= kPfItems &&
+               !wait(&itemempty[k % kPfItems], ((uint32_t)(k / kPfItems) & 1u) ^ 1u))) {
+            give_up();
+            break;
+          }
+          // without a counter there are no more items than CTAs
+          if (lane == 0)
+            i = a.ticket ? (long long)gridDim.x + (long long)atomicAdd(a.ticket, 1ull) : LLONG_MAX;
+          i = __shfl_sync(0xffffffffu, i, 0);
+        }
+        const PfItem it = cur.find(a, i, lane);
+        if (lane == 0) {
+          items[k % kPfItems] = it;
+          mbar_arrive(&itemfull[k % kPfItems]);
+        }
+        __syncwarp();
+        if (it.end) break;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+}  // namespace pkv

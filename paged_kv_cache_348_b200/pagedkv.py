@@ -19,8 +19,8 @@ LIB_PATH = os.path.join(_HERE, "libpagedkv.so")
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_NO_BLOCKS, PA_ERR_NO_MEMORY = \
     0, 1, 2, 3, 4, 5
 PA_F16, PA_BF16 = 0, 1
-DEV_BAD_BLOCK_ID, DEV_BAD_SLOT, DEV_BAD_PAIR, DEV_BAD_CONTEXT_LEN, DEV_TIMEOUT, DEV_BAD_KEEP = (
-    0x1, 0x2, 0x4, 0x8, 0x10, 0x20)
+DEV_BAD_BLOCK_ID, DEV_BAD_SLOT, DEV_BAD_PAIR, DEV_BAD_CONTEXT_LEN, DEV_TIMEOUT, DEV_BAD_KEEP, DEV_BAD_QUERY = (
+    0x1, 0x2, 0x4, 0x8, 0x10, 0x20, 0x40)
 
 # every symbol include/pagedkv.h declares
 EXPORTS = ("pa_version", "pa_status_string", "pa_decode_workspace_bytes", "pa_decode",
@@ -35,7 +35,8 @@ EXPORTS = ("pa_version", "pa_status_string", "pa_decode_workspace_bytes", "pa_de
            "pa_bm_swap_in", "pa_swap_out_blocks", "pa_swap_in_blocks", "pa_cache_append_e4m3_bs",
            "pa_decode_e4m3_bs", "pa_decode_cascade_e4m3_bs", "pa_decode_append_e4m3_bs",
            "pa_check_bounded_waits", "pa_decode_window", "pa_decode_window_e4m3_bs",
-           "pa_compact_tokens", "pa_compact_tokens_e4m3_bs")
+           "pa_compact_tokens", "pa_compact_tokens_e4m3_bs", "pa_prefill_window",
+           "pa_prefill_workspace_bytes")
 
 _lib = None
 _lock = threading.Lock()
@@ -76,6 +77,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.pa_decode_window_e4m3_bs.restype = i32
         L.pa_decode_window_e4m3_bs.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32,
                                                i32, i32, i32, i32, i32, f32, i32, P, sz, P, P]
+        L.pa_prefill_workspace_bytes.restype = sz
+        L.pa_prefill_workspace_bytes.argtypes = []
+        L.pa_prefill_window.restype = i32
+        L.pa_prefill_window.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32,
+                                        i32, i32, i32, f32, i32, P, sz, P, P]
         L.pa_compact_tokens.restype = i32
         L.pa_compact_tokens.argtypes = [P, P, i32, P, i32, P, i32, P, P, P, i32, i32, i32, i32,
                                         i32, i32, i32, i32, i32, P, P]
@@ -548,6 +554,47 @@ def pa_decode_window_e4m3_bs(out, q, k_cache8, v_cache8, k_scales, v_scales, blo
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
         _stream(stream))
     _check(rc, "pa_decode_window_e4m3_bs")
+    return out
+
+
+def pa_prefill_workspace_bytes() -> int:
+    return int(load().pa_prefill_workspace_bytes())
+
+
+def new_prefill_workspace(device=None) -> torch.Tensor:
+    return torch.empty(pa_prefill_workspace_bytes(), dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_prefill_window(out, q, k_cache, v_cache, block_tables, context_lens, q_starts,
+                      window: int, num_sinks: int, scale: float, workspace, status=None,
+                      stream=None):
+    """out[T,Hq,D] <- attention of ragged prompt chunks over the paged cache: the new tokens of
+    sequence s are rows q_starts[s] .. q_starts[s+1]-1 of q (int32 [B+1]), its last cached
+    positions; sliding window and visible first tokens as in pa_decode_window (see
+    pa_prefill_window in include/pagedkv.h)."""
+    _need(q, "q", ndim=3)
+    _need(out, "out", dtype=q.dtype, ndim=3)
+    _need(k_cache, "k_cache", dtype=q.dtype, ndim=4)
+    _need(v_cache, "v_cache", dtype=q.dtype, ndim=4)
+    _need(block_tables, "block_tables", dtype=torch.int32, ndim=2)
+    _need(context_lens, "context_lens", dtype=torch.int32, ndim=1)
+    _need(q_starts, "q_starts", dtype=torch.int32, ndim=1)
+    _need(workspace, "workspace")
+    T, Hq, D = q.shape
+    N, Hkv, bs, D2 = k_cache.shape
+    B = context_lens.shape[0]
+    if out.shape != q.shape or D2 != D or v_cache.shape != k_cache.shape or \
+            block_tables.shape[0] != B or q_starts.shape[0] != B + 1:
+        raise PagedKVError("pa_prefill_window: inconsistent shapes")
+    _here("pa_prefill_window", out, q, k_cache, v_cache, block_tables, context_lens, q_starts,
+          workspace, status)
+    rc = load().pa_prefill_window(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
+        _ptr(q_starts), T, B, Hq, Hkv, D, bs, block_tables.shape[1], N,
+        _whole(window, "window"), _whole(num_sinks, "num_sinks"), float(scale), _dtype_code(q),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+        _stream(stream))
+    _check(rc, "pa_prefill_window")
     return out
 
 

@@ -8,7 +8,7 @@ sum_t p_t (computed per element in 64 bits):
   u_out  half a step of the output type (bf16 2^-8, fp16 2^-11) for the one final rounding;
   u_p    half a step of what P is held in when it meets V (stated by each test);
   d      error of a score in the exponent: D products summed in 32 bits, each step off by at
-         most 2^-23 of the sum of magnitudes S = scale sum_d |q_d k_d|, plus the rounding of
+         most 2^-23 of the sum of magnitudes S = |scale| sum_d |q_d k_d|, plus the rounding of
          the scaled score and exp's own 2^-22: d = (D + 4) 2^-23 max_t S_t + 2^-22; it enters
          numerator and denominator, and twice that covers the reference maximum's rounding;
   n 2^-23  the 32-bit sums over n positions of the numerator and of the denominator;
@@ -54,7 +54,7 @@ def attend(q, k, v, pos, window, num_sinks, scale, u_p, dtype):
         z = torch.where(ok, z, torch.ones_like(z))
         o = e @ vh / z
         a = e @ vh.abs() / z
-        s = scale * (q[:, h].abs() @ kh.abs().T)
+        s = abs(scale) * (q[:, h].abs() @ kh.abs().T)      # magnitudes: a negative scale too
         s = torch.where(see, s, torch.zeros_like(s)).amax(1, keepdim=True)
         d = (D + 4) * 2.0 ** -23 * s + 2.0 ** -22
         cnt = see.sum(1, keepdim=True).double()
