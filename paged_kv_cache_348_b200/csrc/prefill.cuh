@@ -291,22 +291,29 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const bool neg = a.scale_log2 < 0.f;            // the maximum is taken over unscaled scores
     uint32_t sph = 0, oph = 0;
     bool ok = true;
-    PfItem it;
-    for (int k = 0; ok && item_at(k, it); ++k) {
+    for (int k = 0; ok; ++k) {
+      PfItem it;
+      if (!item_at(k, it)) break;
       const int row = it.row0 + sub * kPfSub + r;   // query row of the sequence
       const bool mine = sub * kPfSub + r < it.rows;
       const int token = row / group;
-      // a row past the item's takes part with nothing visible
-      const int p = mine ? it.pos0 + token : -1;
       const bool active = sub * kPfSub < it.rows && it.tiles > 0;
       float m = -INFINITY, l = 0.f;
       if (active) {
-        // tiles [full0, full1) are visible whole to every row of the subtile: after the
-        // last row's window start, up to the first row's own position
-        const int r_last = min(it.rows, (sub + 1) * kPfSub) - 1;
+        auto win0 = [&](int p) {
+          const long long x = (long long)p - a.window + 1;
+          return x > 0 ? (int)x : 0;
+        };
+        // this row sees the positions t <= p with t >= plo or t < num_sinks (a row past the
+        // item's none)
+        const int p = mine ? it.pos0 + token : -1;
+        const int plo = win0(p);
+        // the subtile's first row sees no position past p_first, its last none before lo_last
         const int p_first = it.pos0 + (it.row0 + sub * kPfSub) / group;
-        const int p_last = it.pos0 + (it.row0 + r_last) / group;
-        for (int i = 0; i < it.tiles; ++i) {
+        const int lo_last =
+            win0(it.pos0 + (it.row0 + min(it.rows, (sub + 1) * kPfSub) - 1) / group);
+        const int head = it.head, jump = it.jump, sinks = a.num_sinks, tiles = it.tiles;
+        for (int i = 0; i < tiles; ++i) {
           if (!wait(&sfull[sub], sph)) {
             give_up();
             ok = false;
@@ -325,20 +332,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             for (int j = 0; j < 128; ++j) s[j] ^= 0x80000000u;
           }
           const int v0 = i * kPfKeys;
-          const int t0 = pf_pos(it, v0);
-          // whole: one run of positions, none after the first row's own, none before the
-          // last row's window (or all of them first tokens)
-          const bool whole = (v0 >= it.head || v0 + kPfKeys <= it.head || it.jump == 0) &&
-                             t0 + kPfKeys - 1 <= p_first &&
-                             ((long long)t0 > (long long)p_last - a.window ||
-                              t0 + kPfKeys <= a.num_sinks);
+          const int t0 = v0 < head ? v0 : v0 + jump;
+          // visible whole to every row: one run of positions, none past the first row's own,
+          // none before the last row's window (or all of them first tokens)
+          const bool whole = (v0 >= head || v0 + kPfKeys <= head) && t0 + kPfKeys - 1 <= p_first &&
+                             (t0 >= lo_last || t0 + kPfKeys <= sinks);
           if (!whole) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const int t = pf_pos(it, v0 + 32 * c);
-              const long long w = (long long)p - a.window + 1 - t;
-              const uint32_t see = below32(p + 1 - t) &
-                                   (~below32(w > 32 ? 32 : (w < 0 ? 0 : (int)w)) | below32(a.num_sinks - t));
+              const int v = v0 + 32 * c, t = v < head ? v : v + jump;
+              const uint32_t see = below32(p + 1 - t) & (~below32(plo - t) | below32(sinks - t));
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 if (!(see >> j & 1u)) s[32 * c + j] = 0xff800000u;
@@ -347,9 +350,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           float mx[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            mx[c] = __uint_as_float(s[32 * c]);
+            const uint32_t* x = s + 32 * c;
+            mx[c] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
-            for (int j = 1; j < 32; ++j) mx[c] = fmaxf(mx[c], __uint_as_float(s[32 * c + j]));
+            for (int j = 2; j < 32; j += 2)
+              mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(x[j])), __uint_as_float(x[j + 1]));
           }
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           // the reference moves on a row's first visible tile and past a gap of 2^8
@@ -363,31 +368,31 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             // O so far is against the old reference (its last P V is done: it was issued
             // before the Q K^T whose scores have arrived); before the first P V there is none
             if (i > 0) {
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tO + 32 * c, o);
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                float o[16];
+                tmem_ld16(tO + 16 * c, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                tmem_st32(tO + 32 * c, o);
+                for (int j = 0; j < 16; ++j) o[j] *= alpha;
+                tmem_st16(tO + 16 * c, o);
               }
             }
           }
-          const float ms = m == -INFINITY ? 0.f : m * sc;
+          const float nms = m == -INFINITY ? 0.f : -m * sc;
           float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[32];
+          for (int c = 0; c < 4; ++c) {
+            float pk[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float p0 = ex2(fmaf(__uint_as_float(s[64 * c + 2 * j]), sc, -ms));
-              const float p1 = ex2(fmaf(__uint_as_float(s[64 * c + 2 * j + 1]), sc, -ms));
+            for (int j = 0; j < 16; ++j) {
+              const float p0 = ex2(fmaf(__uint_as_float(s[32 * c + 2 * j]), sc, nms));
+              const float p1 = ex2(fmaf(__uint_as_float(s[32 * c + 2 * j + 1]), sc, nms));
               ls[j & 1] += p0;
               ls[2 + (j & 1)] += p1;
-              pk[j] = pack2<T>(p0, p1);
+              pk[j] = __uint_as_float(pack2<T>(p0, p1));
             }
-            tmem_st32(tS + 32 * c, pk);
+            tmem_st16(tS + 16 * c, pk);
           }
           l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
           tmem_wait_st();
@@ -410,7 +415,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
-        if (active) {
+        if (active) {                               // (warp-uniform)
           tmem_ld32(tO + 32 * c, o);
           tmem_wait_ld();
         }
