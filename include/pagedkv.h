@@ -205,7 +205,7 @@ pa_status pa_decode_window_e4m3_bs(void* out, const void* q, const void* k_cache
  *                  sets PA_DEV_BAD_QUERY
  *   workspace      >= pa_prefill_workspace_bytes() bytes, 16-byte aligned; its contents on
  *                  entry do not matter.  Calls that may run at the same time need one each.
- *   other arguments and errors as for pa_decode (16-bit pools; any number of q heads per kv
+ *   other arguments and errors as for pa_decode (16-bit pools; up to 128 q heads per kv
  *   head).  Weights are rounded to the cache's type before they meet V.
  */
 size_t pa_prefill_workspace_bytes(void);

@@ -128,6 +128,25 @@ bool encode_pool_wide(CUtensorMap* map, const void* base, pa_dtype dtype, int he
   return r == CUDA_SUCCESS;
 }
 
+// 3-D view of q [tokens][heads][head_dim]: boxes of 64 dims x box_heads x box_tokens, the rows
+// (token, head) 128 bytes each, 128-byte swizzle; tokens past the last read as zero.
+bool encode_queries(CUtensorMap* map, const void* base, pa_dtype dtype, int head_dim, int heads,
+                    int tokens, int box_heads, int box_tokens) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  std::memset(map, 0, sizeof(*map));
+  cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)head_dim * 2 * heads};
+  cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = enc(map, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                   3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // Every call gets its own epoch so arrival counters left by earlier calls (or by an
 // aborted one) read as zero; 0 is skipped so a zeroed workspace also reads as zero.
 uint32_t next_epoch() {
@@ -498,6 +517,7 @@ pa_status pa_prefill_window(void* out, const void* q, const void* k_cache, const
   if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
   if (block_size != 1 && block_size != 8 && block_size != 16 && block_size != 32)
     return PA_ERR_UNSUPPORTED;
+  if (num_q_heads / num_kv_heads > pkv::kPfSub) return PA_ERR_UNSUPPORTED;
   // query rows of a sequence, cached positions and pool rows are counted in 32 bits
   if ((long long)total_q * num_q_heads >= (1ll << 31) - 512 ||
       (long long)num_blocks * num_kv_heads * block_size >= (1ll << 31) ||
@@ -542,8 +562,14 @@ pa_status pa_prefill_window(void* out, const void* q, const void* k_cache, const
   a.window = std::min(window, a.ctx_cap);
   a.num_sinks = std::min(num_sinks, a.ctx_cap);
   a.scale_log2 = scale * 1.4426950408889634f;
-  // at most one row tile per 256 query rows and one more per sequence, for every kv head
-  const long long most = ((long long)total_q * a.group / pkv::kPfRows + num_seqs) * num_kv_heads;
+  // query rows as (64 dims, heads of a kv head, new tokens of a subtile) boxes
+  CUtensorMap mq;
+  if (!encode_queries(&mq, q, dtype, head_dim, num_q_heads, total_q, a.group,
+                      pkv::pf_tokens(a.group)))
+    return PA_ERR_CUDA;
+  // at most one item per two subtiles of tokens and one more per sequence, for every kv head
+  const long long most =
+      ((long long)total_q / (2 * pkv::pf_tokens(a.group)) + num_seqs) * num_kv_heads;
   const int grid = (int)std::min<long long>(sms, most);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (most > sms) {                                // CTAs draw items past their first
@@ -551,8 +577,8 @@ pa_status pa_prefill_window(void* out, const void* q, const void* k_cache, const
     if (cudaMemsetAsync(a.ticket, 0, sizeof(*a.ticket), st) != cudaSuccess) return PA_ERR_CUDA;
   }
   return dtype == PA_BF16
-             ? pkv_host::run_prefill_bf16(head_dim, block_size, a, mk, mv, grid, st)
-             : pkv_host::run_prefill_f16(head_dim, block_size, a, mk, mv, grid, st);
+             ? pkv_host::run_prefill_bf16(head_dim, block_size, a, mk, mv, mq, grid, st)
+             : pkv_host::run_prefill_f16(head_dim, block_size, a, mk, mv, mq, grid, st);
 }
 
 pa_status pa_decode_append(void* out, const void* q, void* k_cache, void* v_cache,

@@ -197,36 +197,36 @@ PKV_DECL_WIDE(pkv::kWindow, 64)
 // ---- prompt attention (prefill.cuh); the instances of a type are in prefill_<type>.cu
 template <typename T, int D, int BS>
 pa_status launch_prefill(const pkv::PrefillArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
-                         int grid, cudaStream_t stream) {
+                         const CUtensorMap& mq, int grid, cudaStream_t stream) {
   using L = pkv::PfLayout<D>;
   auto k = pkv::pa_prefill_kernel<T, D, BS>;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynSmem) !=
       cudaSuccess)
     return PA_ERR_CUDA;
-  if (launch(k, dim3(grid), dim3(pkv::kPfThreads), L::kDynSmem, stream, a, mk, mv) != cudaSuccess)
+  if (launch(k, dim3(grid), dim3(pkv::kPfThreads), L::kDynSmem, stream, a, mk, mv, mq) != cudaSuccess)
     return PA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <typename T>
 pa_status dispatch_prefill(int d, int bs, const pkv::PrefillArgs& a, const CUtensorMap& mk,
-                           const CUtensorMap& mv, int grid, cudaStream_t s) {
+                           const CUtensorMap& mv, const CUtensorMap& mq, int grid, cudaStream_t s) {
   switch (d * 100 + bs) {
-    case 6401: return launch_prefill<T, 64, 1>(a, mk, mv, grid, s);
-    case 6408: return launch_prefill<T, 64, 8>(a, mk, mv, grid, s);
-    case 6416: return launch_prefill<T, 64, 16>(a, mk, mv, grid, s);
-    case 6432: return launch_prefill<T, 64, 32>(a, mk, mv, grid, s);
-    case 12801: return launch_prefill<T, 128, 1>(a, mk, mv, grid, s);
-    case 12808: return launch_prefill<T, 128, 8>(a, mk, mv, grid, s);
-    case 12816: return launch_prefill<T, 128, 16>(a, mk, mv, grid, s);
-    case 12832: return launch_prefill<T, 128, 32>(a, mk, mv, grid, s);
+    case 6401: return launch_prefill<T, 64, 1>(a, mk, mv, mq, grid, s);
+    case 6408: return launch_prefill<T, 64, 8>(a, mk, mv, mq, grid, s);
+    case 6416: return launch_prefill<T, 64, 16>(a, mk, mv, mq, grid, s);
+    case 6432: return launch_prefill<T, 64, 32>(a, mk, mv, mq, grid, s);
+    case 12801: return launch_prefill<T, 128, 1>(a, mk, mv, mq, grid, s);
+    case 12808: return launch_prefill<T, 128, 8>(a, mk, mv, mq, grid, s);
+    case 12816: return launch_prefill<T, 128, 16>(a, mk, mv, mq, grid, s);
+    case 12832: return launch_prefill<T, 128, 32>(a, mk, mv, mq, grid, s);
   }
   return PA_ERR_UNSUPPORTED;
 }
 
 pa_status run_prefill_f16(int d, int bs, const pkv::PrefillArgs& a, const CUtensorMap& mk,
-                          const CUtensorMap& mv, int grid, cudaStream_t s);
+                          const CUtensorMap& mv, const CUtensorMap& mq, int grid, cudaStream_t s);
 pa_status run_prefill_bf16(int d, int bs, const pkv::PrefillArgs& a, const CUtensorMap& mk,
-                           const CUtensorMap& mv, int grid, cudaStream_t s);
+                           const CUtensorMap& mv, const CUtensorMap& mq, int grid, cudaStream_t s);
 
 }  // namespace pkv_host

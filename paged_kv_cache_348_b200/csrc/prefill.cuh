@@ -13,9 +13,10 @@
 // the tensor cores 2 x 512 cycles at D = 128 and the special-function units (16 a cycle and
 // SM) 1024, so the two have to run side by side.
 //
-//  * An item is 256 query rows (token-major: row = token * group + head of the group, so the
-//    heads of a kv head share every K/V byte) of one (sequence, kv head), as two subtiles of
-//    128 rows.  While the softmax of one subtile runs, the tensor cores work on the other.
+//  * An item is the query rows of up to 2 floor(128 / group) new tokens of one (sequence, kv
+//    head), as two subtiles of up to 128 rows (token-major: row = token * group + head of the
+//    group, so the heads of a kv head share every K/V byte).  While the softmax of one subtile
+//    runs, the tensor cores work on the other.
 //  * Key tiles are 128 positions.  As in decode.cuh the first tokens are laid directly in
 //    front of the window ("virtual" positions, rounded to 32), so a tile of a few first
 //    tokens is not paid for on its own; positions between are neither loaded nor computed.
@@ -47,9 +48,11 @@ namespace pkv {
 
 constexpr int DEV_BAD_QUERY = 0x40;
 constexpr int kPfSub = 128;                       // query rows of a subtile (MMA M)
-constexpr int kPfRows = 2 * kPfSub;               // query rows of an item
+// new tokens of a subtile: whole tokens, so at most group - 1 of its rows are idle
+__host__ __device__ constexpr int pf_tokens(int group) { return kPfSub / group; }
 constexpr int kPfKeys = 128;                      // positions of a key tile
 constexpr int kPfThreads = 384;
+constexpr int kPfPoly = 4;                        // of 16 pairs of weights, those not on ex2
 constexpr int kPfItems = 2;                       // items a CTA has in flight
 constexpr int kPfAlign = 32;                      // granularity of the virtual positions
 
@@ -72,7 +75,7 @@ struct PrefillArgs {
 struct PfItem {
   int seq, kvh;
   int q0;                                         // first token row of the sequence in q, out
-  int row0, rows;                                 // query rows row0 .. of the sequence
+  int tok0, ntok;                                 // its new tokens tok0 .. of the sequence
   int pos0;                                       // position of the sequence's first new token
   int ctx, w0;                                    // length; first position its queries' windows reach
   int lo, last;                                   // the item's first window position, last position
@@ -87,9 +90,10 @@ struct PfLayout {
   static constexpr int kGroupBytes = kHalves * 1024;           // 8 rows, all halves
   static constexpr int kTileBytes = kHalves * kPfKeys * 128;   // one K or V tile
   static constexpr int kSubBytes = kHalves * kPfSub * 128;     // one subtile of Q
-  static constexpr int kSlots = D == 128 ? 5 : 8;              // K and V tiles in flight
+  static constexpr int kSlots = D == 128 ? 4 : 8;              // K and V tiles in flight
   static constexpr int kQOff = kSlots * kTileBytes;
-  static constexpr int kItemOff = kQOff + 2 * kSubBytes;
+  static constexpr int kOutOff = kQOff + 2 * kSubBytes;        // 2 KB a softmax warp
+  static constexpr int kItemOff = kOutOff + 8 * 2048;
   static constexpr int kBarOff = (kItemOff + kPfItems * (int)sizeof(PfItem) + 15) / 16 * 16;
   // kvfull, kvempty [slots]; itemfull, itemempty [items]; sfull, pfull, odone [2]; qfull, qempty,
   // loaded, drain
@@ -132,7 +136,8 @@ struct PfCursor {
       }
       q0 = b;
       n = e - b;
-      tiles = (int)(((long long)n * a.group + kPfRows - 1) / kPfRows);
+      const int per = 2 * pf_tokens(a.group);
+      tiles = (n + per - 1) / per;
     }
     incl = (long long)tiles * a.num_kv_heads;
 #pragma unroll
@@ -164,9 +169,9 @@ struct PfCursor {
     it.seq = sbase + src;
     const int j = (int)(i - first);
     it.kvh = j % a.num_kv_heads;
-    it.row0 = (nt - 1 - j / a.num_kv_heads) * kPfRows;
-    const int all = nq * a.group;
-    it.rows = all - it.row0 < kPfRows ? all - it.row0 : kPfRows;
+    const int per = 2 * pf_tokens(a.group);
+    it.tok0 = (nt - 1 - j / a.num_kv_heads) * per;
+    it.ntok = nq - it.tok0 < per ? nq - it.tok0 : per;
     it.ctx = clamp_ctx(a.context_lens[it.seq], a.ctx_cap, a.status);
     it.pos0 = it.ctx - nq;
     auto win0 = [&](int p) {
@@ -174,8 +179,8 @@ struct PfCursor {
       return x > 0 ? (int)x : 0;
     };
     it.w0 = win0(it.pos0);
-    it.lo = win0(it.pos0 + it.row0 / a.group);
-    it.last = it.pos0 + (it.row0 + it.rows - 1) / a.group;
+    it.lo = win0(it.pos0 + it.tok0);
+    it.last = it.pos0 + it.tok0 + it.ntok - 1;
     if (it.last >= 0) {
       const int ws = it.lo / kPfAlign * kPfAlign;
       const int hs = a.num_sinks < ws ? (a.num_sinks + kPfAlign - 1) / kPfAlign * kPfAlign : ws;
@@ -190,7 +195,8 @@ struct PfCursor {
 template <typename T, int D, int BS>
 __global__ void __launch_bounds__(kPfThreads, 1)
     pa_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap tmk,
-                      const __grid_constant__ CUtensorMap tmv) {
+                      const __grid_constant__ CUtensorMap tmv,
+                      const __grid_constant__ CUtensorMap tmq) {
   using L = PfLayout<D>;
   constexpr uint32_t kAB = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
   constexpr uint32_t kOCols = 256;                 // O of subtile j from column 256 + 128 j
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       mbar_init(&pfull[i], kPfSub);
       mbar_init(&odone[i], 1);
     }
-    mbar_init(qfull, 32);
+    mbar_init(qfull, 1);
     mbar_init(qempty, 1);
     mbar_init(loaded, 1);
     mbar_init(drain, 1);
@@ -239,6 +245,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   if (threadIdx.x == 32) {
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
+    prefetch_tensormap(&tmq);
   }
   if (warp == 8) {
     tmem_alloc(tmem_slot, 512);
@@ -288,16 +295,19 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // a scale of 0 is taken as 1e-37, which gives the same weights (1) and keeps a masked
     // score's -inf * scale from being NaN
     const float sc = fmaxf(fabsf(a.scale_log2), 1e-37f);
-    const bool neg = a.scale_log2 < 0.f;            // the maximum is taken over unscaled scores
+    const int tps = pf_tokens(group);
+    uint8_t* stage = smem + L::kOutOff + warp * 2048;
+    // this thread's query row: new token jr of the subtile, head gr of the group
+    const int jr = r / group, gr = r - jr * group;
     uint32_t sph = 0, oph = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       PfItem it;
       if (!item_at(k, it)) break;
-      const int row = it.row0 + sub * kPfSub + r;   // query row of the sequence
-      const bool mine = sub * kPfSub + r < it.rows;
-      const int token = row / group;
-      const bool active = sub * kPfSub < it.rows && it.tiles > 0;
+      const int ns = min(it.ntok - sub * tps, tps); // the subtile's tokens
+      const bool mine = jr < ns;
+      const int token = it.tok0 + sub * tps + jr;
+      const bool active = ns > 0 && it.tiles > 0;
       float m = -INFINITY, l = 0.f;
       if (active) {
         auto win0 = [&](int p) {
@@ -308,10 +318,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // item's none)
         const int p = mine ? it.pos0 + token : -1;
         const int plo = win0(p);
-        // the subtile's first row sees no position past p_first, its last none before lo_last
-        const int p_first = it.pos0 + (it.row0 + sub * kPfSub) / group;
-        const int lo_last =
-            win0(it.pos0 + (it.row0 + min(it.rows, (sub + 1) * kPfSub) - 1) / group);
+        // the subtile's first token sees no position past p_first, its last none before lo_last
+        const int p_first = it.pos0 + it.tok0 + sub * tps;
+        const int lo_last = win0(p_first + ns - 1);
         const int head = it.head, jump = it.jump, sinks = a.num_sinks, tiles = it.tiles;
         for (int i = 0; i < tiles; ++i) {
           if (!wait(&sfull[sub], sph)) {
@@ -327,10 +336,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           tmem_ld32(tS + 64, s + 64);
           tmem_ld32(tS + 96, s + 96);
           tmem_wait_ld();
-          if (neg) {
-#pragma unroll
-            for (int j = 0; j < 128; ++j) s[j] ^= 0x80000000u;
-          }
           const int v0 = i * kPfKeys;
           const int t0 = v0 < head ? v0 : v0 + jump;
           // visible whole to every row: one run of positions, none past the first row's own,
@@ -354,9 +359,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             mx[c] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
             for (int j = 2; j < 32; j += 2)
-              mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(x[j])), __uint_as_float(x[j + 1]));
+              mx[c] = max3(mx[c], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
           }
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           // the reference moves on a row's first visible tile and past a gap of 2^8
           const bool move = mt > m && (m == -INFINITY || (mt - m) * sc > kRescaleLog2);
           if (__any_sync(0xffffffffu, move)) {
@@ -380,21 +385,39 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
           }
           const float nms = m == -INFINITY ? 0.f : -m * sc;
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          const uint64_t sc2 = pack_f2(sc, sc), nms2 = pack_f2(nms, nms);
+          uint64_t ls[2] = {0ull, 0ull};
+          // weights of 32 positions: of every 16 pairs kPoly on the FMA units, which a masked
+          // tile's -inf must not take (it would leave 2^-126)
+          auto weights = [&](int c, auto poly) {
+            constexpr int kPoly = decltype(poly)::value;
             float pk[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const float p0 = ex2(fmaf(__uint_as_float(s[32 * c + 2 * j]), sc, nms));
-              const float p1 = ex2(fmaf(__uint_as_float(s[32 * c + 2 * j + 1]), sc, nms));
-              ls[j & 1] += p0;
-              ls[2 + (j & 1)] += p1;
-              pk[j] = __uint_as_float(pack2<T>(p0, p1));
+              const uint64_t x = fma_f2(pack_f2(__uint_as_float(s[32 * c + 2 * j]),
+                                                __uint_as_float(s[32 * c + 2 * j + 1])),
+                                        sc2, nms2);
+              float2 w;
+              if (j * kPoly / 16 != (j + 1) * kPoly / 16) {
+                w = ex2_poly_f2(x);
+              } else {
+                const float2 y = unpack_f2(x);
+                w = make_float2(ex2(y.x), ex2(y.y));
+              }
+              ls[j & 1] = add_f2(ls[j & 1], pack_f2(w.x, w.y));
+              pk[j] = __uint_as_float(pack2<T>(w.x, w.y));
             }
             tmem_st16(tS + 16 * c, pk);
+          };
+          if (whole) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) weights(c, std::integral_constant<int, kPfPoly>{});
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) weights(c, std::integral_constant<int, 0>{});
           }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          const float2 l2 = unpack_f2(add_f2(ls[0], ls[1]));
+          l += l2.x + l2.y;
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&pfull[sub]);
@@ -407,31 +430,46 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         oph ^= 1u;
         tc_fence_after();
       }
-      // output rows; a row that sees nothing is zero
-      const float inv = 1.f / l;
-      T* orow = static_cast<T*>(a.out) +
-                (((long long)it.q0 + token) * a.num_q_heads + (long long)it.kvh * group +
-                 (row - token * group)) * D;
+      // output rows; a row that sees nothing is zero.  A thread holds a row of O, so 32
+      // columns at a time go through the warp's staging area and out as 64 contiguous bytes of
+      // each row (a store per thread and row would touch 32 lines an instruction)
+      if (ns > 0) {
+        const float inv = 1.f / l;
+        const int orow = mine ? (it.q0 + token) * a.num_q_heads + it.kvh * group + gr : -1;
+        const int u = lane & 3;
+        int rows[4];                                // output rows that this lane stores
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (active) {                               // (warp-uniform)
-          tmem_ld32(tO + 32 * c, o);
-          tmem_wait_ld();
-        }
-        if (mine) {
+        for (int x = 0; x < 4; ++x) rows[x] = __shfl_sync(0xffffffffu, orow, x * 8 + (lane >> 2));
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (active) {                             // (warp-uniform)
+            tmem_ld32(tO + 32 * c, o);
+            tmem_wait_ld();
+          }
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int x = 0; x < 4; ++x) {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               w[j] = l == 0.f ? 0u
-                              : pack2<T>(__uint_as_float(o[8 * u + 2 * j]) * inv,
-                                         __uint_as_float(o[8 * u + 2 * j + 1]) * inv);
-            *reinterpret_cast<uint4*>(orow + 32 * c + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
+                              : pack2<T>(__uint_as_float(o[8 * x + 2 * j]) * inv,
+                                         __uint_as_float(o[8 * x + 2 * j + 1]) * inv);
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((x ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int rr = x * 8 + (lane >> 2);
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * 64 +
+                                                            ((u ^ ((rr >> 1) & 3)) << 4));
+            if (rows[x] >= 0)
+              *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)rows[x] * D + 32 * c +
+                                        8 * u) = w;
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       tc_fence_before();                            // O is read before the next item's P V
       item_done(k);
@@ -440,7 +478,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
       // ============================== tensor-core issue ==============================
-      const uint32_t idesc_qk = idesc_f16(kAB, 0u, 0u, kPfSub, kPfKeys);
+      // a negative scale: -Q in its place, so that the softmax may take maxima of scores
+      const uint32_t idesc_qk = idesc_f16(kAB, 0u, 0u, kPfSub, kPfKeys) |
+                                (a.scale_log2 < 0.f ? kIdescNegateA : 0u);
       const uint32_t idesc_pv = idesc_f16(kAB, 0u, 1u, kPfSub, (uint32_t)D);
       const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16u, 1024u);
       const uint64_t dk0 = smem_desc_sw128(smem_u32(smem), 16u, L::kGroupBytes);
@@ -451,7 +491,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       PfItem it;
       for (int k = 0; ok && item_at(k, it); ++k) {
         if (lane == 0 && it.tiles > 0) {
-          const int nsub = it.rows > kPfSub ? 2 : 1;
+          const int nsub = it.ntok > pf_tokens(group) ? 2 : 1;
           auto tile = [&](uint32_t fill) {          // a K or V tile has landed
             const bool got = wait(&kvfull[fill % L::kSlots], (fill / L::kSlots) & 1u);
             fence_proxy_async_smem();               // parts may have come by cp.async
@@ -649,26 +689,26 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             break;
           }
           ++used;
-          constexpr int CPR = D / 8;
-          const T* base = static_cast<const T*>(a.q) + (long long)it.q0 * a.num_q_heads * D +
-                          (long long)it.kvh * group * D;
-          const int rows = it.rows > kPfSub ? kPfRows : kPfSub;
-          constexpr int kStep = 32 / CPR;           // rows the warp covers at a time
-          const int ch = lane % CPR;
-          for (int x = lane / CPR; x < rows; x += kStep) {
-            const bool in = x < it.rows;
-            const int row = it.row0 + (in ? x : 0), token = row / group;
-            const T* src = base + ((long long)token * a.num_q_heads + (row - token * group)) * D;
-            const int xr = x & (kPfSub - 1);
-            cp_async_16_zfill(sQ + (x / kPfSub) * L::kSubBytes + (ch >> 3) * (kPfSub * 128) +
-                                  xr * 128 + (((ch & 7) ^ (xr & 7)) << 4),
-                              src + ch * 8, in ? 16u : 0u);
+          // a subtile's tokens with the heads of this kv head: one box per 64 dims, its rows
+          // token-major (tokens behind the sequence's last give rows that nobody writes)
+          const int tps = pf_tokens(group), nsub = it.ntok > tps ? 2 : 1;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(qfull, (uint32_t)(nsub * L::kHalves * tps * group * 128));
+            for (int x = 0; x < nsub * L::kHalves; ++x) {
+              const int j = x / L::kHalves, hf = x % L::kHalves;
+              tma_load_3d(sQ + j * L::kSubBytes + hf * (kPfSub * 128), &tmq, qfull, hf * 64,
+                          it.kvh * group, it.q0 + it.tok0 + j * tps);
+            }
           }
-          cp_async_mbar_arrive_noinc(qfull);
+          __syncwarp();
         }
         item_done(k);
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      // a copy still in flight (only after a failed wait) lands before the memory goes
+      if (*abort_flag && used > 0) {
+        int no_abort = 0;
+        mbar_wait_bounded(qfull, (uint32_t)(used - 1) & 1u, &no_abort, kWaitLimitNs);
+      }
     } else {
       // ============================== items ==============================
       // The first item is the CTA's index; the later ones are drawn from a counter shared by

@@ -5,8 +5,8 @@
 namespace pkv_host {
 
 pa_status run_prefill_f16(int d, int bs, const pkv::PrefillArgs& a, const CUtensorMap& mk,
-                         const CUtensorMap& mv, int grid, cudaStream_t s) {
-  return dispatch_prefill<__half>(d, bs, a, mk, mv, grid, s);
+                         const CUtensorMap& mv, const CUtensorMap& mq, int grid, cudaStream_t s) {
+  return dispatch_prefill<__half>(d, bs, a, mk, mv, mq, grid, s);
 }
 
 }  // namespace pkv_host

@@ -116,6 +116,15 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
@@ -212,6 +221,54 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+
+// Maximum of three.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two binary32 values in one 64-bit register, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pack_f2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpack_f2(uint64_t x) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(x));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 2^x of both values on the FMA units, beside the special-function units that ex2 uses:
+// x = n + f with n the nearest whole number (added to 1.5 * 2^23 it sits in the low bits), 2^f
+// on [-1/2, 1/2] by the degree-4 polynomial of least maximum relative error (2.6e-6; fitted
+// with the exchange algorithm of Remez), n added to the exponent.  For x in [-126, 127);
+// smaller values are taken as -126.
+__device__ __forceinline__ float2 ex2_poly_f2(uint64_t x) {
+  const float2 c = unpack_f2(x);
+  x = pack_f2(fmaxf(c.x, -126.f), fmaxf(c.y, -126.f));
+  constexpr float kRound = 12582912.f;
+  const uint64_t t = add_f2(x, pack_f2(kRound, kRound));
+  const uint64_t f = fma_f2(add_f2(t, pack_f2(-kRound, -kRound)), pack_f2(-1.f, -1.f), x);
+  uint64_t p = pack_f2(0.009570102207362652f, 0.009570102207362652f);
+  p = fma_f2(p, f, pack_f2(0.05591785907745361f, 0.05591785907745361f));
+  p = fma_f2(p, f, pack_f2(0.240247443318367f, 0.240247443318367f));
+  p = fma_f2(p, f, pack_f2(0.6931217908859253f, 0.6931217908859253f));
+  p = fma_f2(p, f, pack_f2(0.9999992847442627f, 0.9999992847442627f));
+  const float2 n = unpack_f2(t), r = unpack_f2(p);
+  return make_float2(__uint_as_float(__float_as_uint(r.x) + (__float_as_uint(n.x) << 23)),
+                     __uint_as_float(__float_as_uint(r.y) + (__float_as_uint(n.y) << 23)));
+}
 
 // ---------------------------------------------------------------- tcgen05 (5th-generation tensor cores)
 // Tensor-memory addresses: bits 31..16 = lane (data path), bits 15..0 = column.
@@ -325,6 +382,7 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
+constexpr uint32_t kIdescNegateA = 1u << 13;      // the product of -A and B
 // Instruction descriptor of kind::f16 with f32 accumulation: operand type (0 f16, 1 bf16),
 // major-ness of A and B (0 K-major, 1 MN-major), M and N.
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t ab_type, uint32_t a_mn, uint32_t b_mn,
