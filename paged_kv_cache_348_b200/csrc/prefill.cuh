@@ -52,7 +52,7 @@ constexpr int kPfSub = 128;                       // query rows of a subtile (MM
 __host__ __device__ constexpr int pf_tokens(int group) { return kPfSub / group; }
 constexpr int kPfKeys = 128;                      // positions of a key tile
 constexpr int kPfThreads = 384;
-constexpr int kPfPoly = 4;                        // of 16 pairs of weights, those not on ex2
+constexpr int kPfPoly = 2;                        // of 16 pairs of weights, those not on ex2
 constexpr int kPfItems = 2;                       // items a CTA has in flight
 constexpr int kPfAlign = 32;                      // granularity of the virtual positions
 
@@ -109,6 +109,14 @@ struct PfLayout {
 // Position of virtual position v of an item.
 __device__ __forceinline__ int pf_pos(const PfItem& it, int v) {
   return v < it.head ? v : v + it.jump;
+}
+
+// x = -inf where `keep` is 0, in place (a conditional expression made the compiler copy every
+// score of an unmasked tile too)
+__device__ __forceinline__ void mask_to_ninf(uint32_t& x, uint32_t keep) {
+  asm("{\n\t.reg .pred p;\n\tsetp.eq.b32 p, %1, 0;\n\t@p mov.b32 %0, 0xff800000;\n\t}"
+      : "+r"(x)
+      : "r"(keep));
 }
 
 // bits r < n (n clamped to 0..32)
@@ -348,8 +356,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               const int v = v0 + 32 * c, t = v < head ? v : v + jump;
               const uint32_t see = below32(p + 1 - t) & (~below32(plo - t) | below32(sinks - t));
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(see >> j & 1u)) s[32 * c + j] = 0xff800000u;
+              for (int j = 0; j < 32; ++j) mask_to_ninf(s[32 * c + j], see & (1u << j));
             }
           }
           float mx[4];
