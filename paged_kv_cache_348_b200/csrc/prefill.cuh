@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kSlots; ++i) {
-      mbar_init(&kvfull[i], 33);                   // expect_tx and 32 cp.async arrivals
+      mbar_init(&kvfull[i], 1);
       mbar_init(&kvempty[i], 1);
     }
     for (int i = 0; i < kPfItems; ++i) {
@@ -500,10 +500,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (lane == 0 && it.tiles > 0) {
           const int nsub = it.ntok > pf_tokens(group) ? 2 : 1;
           auto tile = [&](uint32_t fill) {          // a K or V tile has landed
-            const bool got = wait(&kvfull[fill % L::kSlots], (fill / L::kSlots) & 1u);
-            fence_proxy_async_smem();               // parts may have come by cp.async
-            tc_fence_after();
-            return got;
+            return wait(&kvfull[fill % L::kSlots], (fill / L::kSlots) & 1u);
           };
           auto qk = [&](int j, uint32_t fill) {
             const uint32_t so = (fill % L::kSlots) * L::kTileBytes;
@@ -526,7 +523,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           for (int i = 0; ok && i < it.tiles; ++i) {
             const uint32_t fv = f + 2 * i + 1, fk = f + 2 * i + 2;
             const bool more = i + 1 < it.tiles;
-            ok = tile(fv) && (!more || tile(fk));
+            ok = tile(fv);
             for (int j = 0; ok && j < nsub; ++j) {
               if (!wait(&pfull[j], pph[j])) {
                 ok = false;
@@ -543,6 +540,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               if (!more) tc_commit(&odone[j]);
               if (j == nsub - 1) tc_commit(&kvempty[fv % L::kSlots]);
               if (more) {
+                if (j == 0 && !tile(fk)) {
+                  ok = false;
+                  break;
+                }
                 qk(j, fk);
                 if (j == nsub - 1) {
                   tc_commit(&kvempty[fk % L::kSlots]);
@@ -629,27 +630,43 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               // K boxes that nothing needs keep what the slot held (their scores are masked);
               // V boxes become zeros
               const bool box = lane < kBoxes && (kv ? !patch : load_k);
+              // rows copied one by one: stored by this warp and fenced against the tensor cores'
+              // reads before the tile's barrier is armed (the tensor-core warp would otherwise
+              // pay for a fence at every tile)
+              unsigned todo = kv ? __ballot_sync(0xffffffffu, patch) : 0u;
+              if (todo) {
+                while (todo) {
+                  const int b = __ffs(todo) - 1;
+                  todo &= todo - 1;
+                  const int t = pf_pos(it, i * kPfKeys + b * H);
+                  const long long yb = __shfl_sync(0xffffffffu, y[0], b);
+                  constexpr int CPR = D / 8;        // 16-byte pieces of a row
+                  constexpr int kN = H * CPR / 32;
+                  uint4 w[kN];
+#pragma unroll
+                  for (int u = 0; u < kN; ++u) {
+                    const int rr = (u * 32 + lane) / CPR, ch = lane % CPR;
+                    w[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (seen(t + rr))
+                      w[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v_cache) +
+                                                             (yb + rr) * D + ch * 8);
+                  }
+#pragma unroll
+                  for (int u = 0; u < kN; ++u) {
+                    const int rr = (u * 32 + lane) / CPR, ch = lane % CPR, tr = b * H + rr;
+                    *reinterpret_cast<uint4*>(dst + (tr >> 3) * L::kGroupBytes + (ch >> 3) * 1024 +
+                                              (tr & 7) * 128 + (((ch & 7) ^ (tr & 7)) << 4)) = w[u];
+                  }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+              }
               const unsigned n = __popc(__ballot_sync(0xffffffffu, box));
               if (lane == 0) mbar_arrive_expect_tx(&kvfull[sl], n * kBoxBytes);
               __syncwarp();
               if (box)
                 tma_load_4d(dst + lane * (H / 8) * L::kGroupBytes, map, &kvfull[sl], y[0] >> 3,
                             policy);
-              unsigned todo = kv ? __ballot_sync(0xffffffffu, patch) : 0u;
-              while (todo) {
-                const int b = __ffs(todo) - 1;
-                todo &= todo - 1;
-                const int t = pf_pos(it, i * kPfKeys + b * H);
-                const long long yb = __shfl_sync(0xffffffffu, y[0], b);
-                constexpr int CPR = D / 8;          // 16-byte pieces of a row
-                for (int x = lane; x < H * CPR; x += 32) {
-                  const int rr = x / CPR, ch = x % CPR, tr = b * H + rr;
-                  cp_async_16_zfill(dst + (tr >> 3) * L::kGroupBytes + (ch >> 3) * 1024 +
-                                        (tr & 7) * 128 + (((ch & 7) ^ (tr & 7)) << 4),
-                                    static_cast<const T*>(a.v_cache) + (yb + rr) * D + ch * 8,
-                                    seen(t + rr) ? 16u : 0u);
-                }
-              }
             } else {
               // four rows a gather load, one 128-byte half of each
               if (lane == 0) mbar_arrive_expect_tx(&kvfull[sl], L::kTileBytes);
@@ -670,7 +687,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                             &kvfull[sl], hf * 64, z[0], z[1], z[2], z[3], policy);
               }
             }
-            cp_async_mbar_arrive_noinc(&kvfull[sl]);
           }
 #pragma unroll
           for (int x = 0; x < kE; ++x) cur[x] = nxt[x];
@@ -679,7 +695,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (lane == 0) mbar_arrive(loaded);
       }
       // copies still in flight (only after a failed wait) land before the CTA's memory goes
-      asm volatile("cp.async.wait_all;" ::: "memory");
       if (!ok || *abort_flag) {
         int no_abort = 0;
         for (uint32_t g = f > L::kSlots ? f - L::kSlots : 0; g < f; ++g)

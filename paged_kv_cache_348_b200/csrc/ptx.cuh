@@ -140,13 +140,6 @@ __device__ __forceinline__ void cp_async_16(void* dst, const void* src, uint64_t
                : "memory");
 }
 
-// the same with zeros in place of the source's bytes when src_bytes is 0 (16: a plain copy)
-__device__ __forceinline__ void cp_async_16_zfill(void* dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(src_bytes)
-               : "memory");
-}
-
 __device__ __forceinline__ uint64_t policy_evict_normal() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
