@@ -276,16 +276,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_wait_bounded(bar, parity, abort_flag, kWaitLimitNs);
   };
-  // item k of this CTA, or false at the end of the launch (or of patience); item_done hands
-  // its slot back
-  auto item_at = [&](int k, PfItem& it) {
+  // whether there is an item k of this CTA (false at the end of the launch or of patience);
+  // its fields are read from its slot, which item_done hands back
+  auto item_at = [&](int k) {
     const int sl = k % kPfItems;
     if (!wait(&itemfull[sl], (uint32_t)(k / kPfItems) & 1u)) {
       give_up();
       return false;
     }
-    it = items[sl];
-    return it.end == 0;
+    return items[sl].end == 0;
   };
   auto item_done = [&](int k) {
     __syncwarp();
@@ -310,8 +309,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     uint32_t sph = 0, oph = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      PfItem it;
-      if (!item_at(k, it)) break;
+      if (!item_at(k)) break;
+      const PfItem& it = items[k % kPfItems];
       const int ns = min(it.ntok - sub * tps, tps); // the subtile's tokens
       const bool mine = jr < ns;
       const int token = it.tok0 + sub * tps + jr;
@@ -485,84 +484,109 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
       // ============================== tensor-core issue ==============================
+      // The whole warp walks the tiles and one elected lane issues, in branches on elect.sync's
+      // own predicate: operands then sit in uniform registers and the instructions follow each
+      // other at the tensor cores' pace (64 cycles for 128 x 128 x 16).  Behind a predicate or a
+      // branch on the lane number the same instructions took 72 to 100 cycles each to issue.
+      const bool one = elect_one();
+      const uint32_t idesc_pv = idesc_f16(kAB, 0u, 1u, kPfSub, (uint32_t)D);
       // a negative scale: -Q in its place, so that the softmax may take maxima of scores
       const uint32_t idesc_qk = idesc_f16(kAB, 0u, 0u, kPfSub, kPfKeys) |
                                 (a.scale_log2 < 0.f ? kIdescNegateA : 0u);
-      const uint32_t idesc_pv = idesc_f16(kAB, 0u, 1u, kPfSub, (uint32_t)D);
       const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16u, 1024u);
       const uint64_t dk0 = smem_desc_sw128(smem_u32(smem), 16u, L::kGroupBytes);
       const uint64_t dv0 = smem_desc_sw128(smem_u32(smem), 1024u, L::kGroupBytes);
-      auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
-      uint32_t f = 0, qph = 0, pph[2] = {0, 0};     // K/V tiles taken; phases
-      bool ok = true;
-      PfItem it;
-      for (int k = 0; ok && item_at(k, it); ++k) {
-        if (lane == 0 && it.tiles > 0) {
-          const int nsub = it.ntok > pf_tokens(group) ? 2 : 1;
-          auto tile = [&](uint32_t fill) {          // a K or V tile has landed
-            return wait(&kvfull[fill % L::kSlots], (fill / L::kSlots) & 1u);
-          };
-          auto qk = [&](int j, uint32_t fill) {
-            const uint32_t so = (fill % L::kSlots) * L::kTileBytes;
+      constexpr uint32_t kTile16 = L::kTileBytes / 16;
+      // slot and phase of the next V tile (fill 1, 3, ..) and the next K tile (0, 2, ..)
+      uint32_t sk = 0, kph = 0, sv = 1, vph = 0, qph = 0, pph0 = 0, pph1 = 0;
+      auto next = [](uint32_t& sl, uint32_t& ph) {  // two fills on
+        sl += 2;
+        if (sl >= (uint32_t)L::kSlots) {
+          sl -= (uint32_t)L::kSlots;
+          ph ^= 1u;
+        }
+      };
+      auto qk = [&](auto j_) {
+        constexpr int j = decltype(j_)::value;
+        const uint64_t dk = dk0 + sk * kTile16;
+        if (!one) return;
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = (ks & 3) * 32;
-              tc_mma_f16(tbase + (uint32_t)(j * 128),
-                         adv(dq0, j * L::kSubBytes + (ks >> 2) * (kPfSub * 128) + off),
-                         adv(dk0, so + (ks >> 2) * 1024 + off), idesc_qk, ks > 0);
-            }
-            tc_commit(&sfull[j]);
-          };
-          ok = wait(qfull, qph) && tile(f);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks & 3) * 32;
+          tc_mma_f16(tbase + (uint32_t)(j * 128),
+                     dq0 + ((j * L::kSubBytes + (ks >> 2) * (kPfSub * 128) + off) >> 4),
+                     dk + (((ks >> 2) * 1024 + off) >> 4), idesc_qk, ks > 0);
+        }
+        tc_commit(&sfull[j]);
+      };
+      auto pv = [&](auto j_, bool more) {
+        constexpr int j = decltype(j_)::value;
+        const uint64_t dv = dv0 + sv * kTile16;
+        if (!one) return;
+#pragma unroll
+        for (int kk = 0; kk < kPfKeys / 16; ++kk)
+          tc_mma_f16_ts(tbase + kOCols + (uint32_t)(j * 128), tbase + (uint32_t)(j * 128 + kk * 8),
+                        dv + ((kk * 2 * L::kGroupBytes) >> 4), idesc_pv, more || kk > 0);
+      };
+      // (votes and reductions, so that the compiler sees one value for the warp)
+      auto got = [](bool x) { return (bool)__all_sync(0xffffffffu, x); };
+      std::integral_constant<int, 0> A;
+      std::integral_constant<int, 1> B;
+      bool ok = true;
+      for (int k = 0; ok && got(item_at(k)); ++k) {
+        const PfItem& it = items[k % kPfItems];
+        const int tiles = __reduce_max_sync(0xffffffffu, it.tiles);
+        const bool two = __any_sync(0xffffffffu, it.ntok > pf_tokens(group));
+        if (tiles > 0) {
+          ok = got(wait(qfull, qph)) && got(wait(&kvfull[sk], kph));
           qph ^= 1u;
           if (ok) {
-            for (int j = 0; j < nsub; ++j) qk(j, f);
-            tc_commit(&kvempty[f % L::kSlots]);
-            if (it.tiles == 1) tc_commit(qempty);
+            tc_fence_after();
+            qk(A);
+            if (two) qk(B);
+            if (one) tc_commit(&kvempty[sk]);
+            if (tiles == 1 && one) tc_commit(qempty);
+            next(sk, kph);
           }
-          for (int i = 0; ok && i < it.tiles; ++i) {
-            const uint32_t fv = f + 2 * i + 1, fk = f + 2 * i + 2;
-            const bool more = i + 1 < it.tiles;
-            ok = tile(fv);
-            for (int j = 0; ok && j < nsub; ++j) {
-              if (!wait(&pfull[j], pph[j])) {
-                ok = false;
-                break;
-              }
-              pph[j] ^= 1u;
+          for (int i = 0; ok && i < tiles; ++i) {
+            const bool more = i + 1 < tiles;
+            ok = got(wait(&kvfull[sv], vph)) && got(wait(&pfull[0], pph0));
+            if (!ok) break;
+            pph0 ^= 1u;
+            tc_fence_after();
+            pv(A, i > 0);
+            if (!more && one) tc_commit(&odone[0]);
+            if (more) {
+              ok = got(wait(&kvfull[sk], kph));
+              if (!ok) break;
               tc_fence_after();
-              const uint32_t so = (fv % L::kSlots) * L::kTileBytes;
-#pragma unroll
-              for (int kk = 0; kk < kPfKeys / 16; ++kk)
-                tc_mma_f16_ts(tbase + kOCols + (uint32_t)(j * 128),
-                              tbase + (uint32_t)(j * 128 + kk * 8),
-                              adv(dv0, so + kk * 2 * L::kGroupBytes), idesc_pv, i > 0 || kk > 0);
-              if (!more) tc_commit(&odone[j]);
-              if (j == nsub - 1) tc_commit(&kvempty[fv % L::kSlots]);
-              if (more) {
-                if (j == 0 && !tile(fk)) {
-                  ok = false;
-                  break;
-                }
-                qk(j, fk);
-                if (j == nsub - 1) {
-                  tc_commit(&kvempty[fk % L::kSlots]);
-                  if (i + 2 == it.tiles) tc_commit(qempty);
-                }
-              }
+              qk(A);
+            }
+            if (two) {
+              ok = got(wait(&pfull[1], pph1));
+              if (!ok) break;
+              pph1 ^= 1u;
+              tc_fence_after();
+              pv(B, i > 0);
+              if (!more && one) tc_commit(&odone[1]);
+              if (one) tc_commit(&kvempty[sv]);
+              if (more) qk(B);
+            } else {
+              if (one) tc_commit(&kvempty[sv]);
+            }
+            next(sv, vph);
+            if (more) {
+              if (one) tc_commit(&kvempty[sk]);
+              next(sk, kph);
+              if (i + 2 == tiles && one) tc_commit(qempty);
             }
           }
-          f += 2 * it.tiles;
-          if (!ok) {
-            *abort_flag = 1;
-            if (a.status) atomicOr(a.status, DEV_TIMEOUT);
-          }
+          if (!ok) give_up();
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
         item_done(k);
       }
-      if (lane == 0) {
-        // nothing issued here may still run when tensor memory is released
+      // nothing issued here may still run when tensor memory is released
+      if (one) {
         tc_commit(drain);
         int no_abort = 0;
         mbar_wait_bounded(drain, 0u, &no_abort, kWaitLimitNs);
@@ -574,8 +598,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const int rows_total = a.num_blocks * Hkv * BS;
       uint32_t f = 0;
       bool ok = true;
-      PfItem it;
-      for (int k = 0; ok && item_at(k, it); ++k) {
+      for (int k = 0; ok && item_at(k); ++k) {
+        const PfItem it = items[k % kPfItems];
         const int32_t* trow = a.block_tables + (long long)it.seq * a.max_blocks;
         const int S = a.num_sinks;
         // needed by this item; sure: no position of t .. t+n-1 is hidden from every query of
@@ -703,8 +727,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     } else if (warp == 10) {
       // ============================== query rows ==============================
       int used = 0;
-      PfItem it;
-      for (int k = 0; item_at(k, it); ++k) {
+      for (int k = 0; item_at(k); ++k) {
+        const PfItem& it = items[k % kPfItems];
         if (it.tiles > 0) {
           if (used > 0 && !wait(qempty, (uint32_t)(used - 1) & 1u)) {
             give_up();
