@@ -20,10 +20,10 @@
 //  * Key tiles are 128 positions.  As in decode.cuh the first tokens are laid directly in
 //    front of the window ("virtual" positions, rounded to 32), so a tile of a few first
 //    tokens is not paid for on its own; positions between are neither loaded nor computed.
-//  * Tensor memory, 512 columns: S of either subtile (128 columns each) and O of either.
-//    P goes over the S it came from, 16 bits a value, and is the A operand of P V from
-//    there.  Tensor-core operations of one thread execute in order, so Q K^T of the next key
-//    tile may overwrite P right behind the P V that reads it.
+//  * Tensor memory, 512 columns: one S (128 columns) that the two subtiles use in turn, P of
+//    either (64 columns, 16 bits a value, the A operand of P V from there) and O of either
+//    (128).  A subtile's scores are taken to registers at once, so the next Q K^T need not
+//    wait for its exponentials, and the tensor cores always have a product to run.
 //  * Softmax: one thread per query row, base 2 in 32 bits, so a row's maximum and sum need
 //    no exchange.  The reference maximum moves only when a score passes it by 2^8 (O is
 //    then rescaled in tensor memory); after a row's first key tile that is rare.  The row
@@ -95,9 +95,9 @@ struct PfLayout {
   static constexpr int kOutOff = kQOff + 2 * kSubBytes;        // 2 KB a softmax warp
   static constexpr int kItemOff = kOutOff + 8 * 2048;
   static constexpr int kBarOff = (kItemOff + kPfItems * (int)sizeof(PfItem) + 15) / 16 * 16;
-  // kvfull, kvempty [slots]; itemfull, itemempty [items]; sfull, pfull, odone [2]; qfull, qempty,
-  // loaded, drain
-  static constexpr int kNumBars = 2 * kSlots + 2 * kPfItems + 6 + 4;
+  // kvfull, kvempty [slots]; itemfull, itemempty [items]; sfull, pfull, sfree, pvdone [2]; qfull,
+  // qempty, loaded, drain
+  static constexpr int kNumBars = 2 * kSlots + 2 * kPfItems + 8 + 4;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;      // tmem base, abort flag
   static constexpr int kBytes = kMiscOff + 16;
   static constexpr int kDynSmem = kBytes + 1024;
@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                       const __grid_constant__ CUtensorMap tmq) {
   using L = PfLayout<D>;
   constexpr uint32_t kAB = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
-  constexpr uint32_t kOCols = 256;                 // O of subtile j from column 256 + 128 j
+  // tensor memory: S from column 0, P of subtile j from 128 + 64 j, O from 256 + 128 j
+  constexpr uint32_t kPCols = 128, kOCols = 256;
   constexpr int kItemUsers = 8 + 1 + 1 + 1;        // warps that read an item
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -220,8 +221,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   uint64_t* itemempty = itemfull + kPfItems;
   uint64_t* sfull = itemempty + kPfItems;
   uint64_t* pfull = sfull + 2;
-  uint64_t* odone = pfull + 2;
-  uint64_t* qfull = odone + 2;
+  uint64_t* sfree = pfull + 2;
+  uint64_t* pvdone = sfree + 2;
+  uint64_t* qfull = pvdone + 2;
   uint64_t* qempty = qfull + 1;
   uint64_t* loaded = qempty + 1;
   uint64_t* drain = loaded + 1;
@@ -241,7 +243,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], kPfSub);
-      mbar_init(&odone[i], 1);
+      mbar_init(&pvdone[i], 1);
+      mbar_init(&sfree[i], 4);
     }
     mbar_init(qfull, 1);
     mbar_init(qempty, 1);
@@ -297,7 +300,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int sub = warp >> 2;
     const int r = (warp & 3) * 32 + lane;           // row of the subtile = lane of tensor memory
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tbase + lanes + (uint32_t)(sub * 128);
+    const uint32_t tS = tbase + lanes;
+    const uint32_t tP = tbase + lanes + kPCols + (uint32_t)(sub * 64);
     const uint32_t tO = tbase + lanes + kOCols + (uint32_t)(sub * 128);
     // a scale of 0 is taken as 1e-37, which gives the same weights (1) and keeps a masked
     // score's -inf * scale from being NaN
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     uint8_t* stage = smem + L::kOutOff + warp * 2048;
     // this thread's query row: new token jr of the subtile, head gr of the group
     const int jr = r / group, gr = r - jr * group;
-    uint32_t sph = 0, oph = 0;
+    uint32_t sph = 0, vph = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!item_at(k)) break;
@@ -343,6 +347,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           tmem_ld32(tS + 64, s + 64);
           tmem_ld32(tS + 96, s + 96);
           tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfree[sub]);
           const int v0 = i * kPfKeys;
           const int t0 = v0 < head ? v0 : v0 + jump;
           // visible whole to every row: one run of positions, none past the first row's own,
@@ -370,14 +377,23 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           // the reference moves on a row's first visible tile and past a gap of 2^8
           const bool move = mt > m && (m == -INFINITY || (mt - m) * sc > kRescaleLog2);
+          // the P V of the tile before has read P and is done with O
+          if (i > 0) {
+            if (!wait(&pvdone[sub], vph)) {
+              give_up();
+              ok = false;
+              break;
+            }
+            vph ^= 1u;
+            tc_fence_after();
+          }
           if (__any_sync(0xffffffffu, move)) {
             const float alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2((m - mt) * sc));
             if (move) {
               l *= alpha;
               m = mt;
             }
-            // O so far is against the old reference (its last P V is done: it was issued
-            // before the Q K^T whose scores have arrived); before the first P V there is none
+            // O so far is against the old reference; before the first P V there is none
             if (i > 0) {
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
@@ -413,7 +429,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               ls[j & 1] = add_f2(ls[j & 1], pack_f2(w.x, w.y));
               pk[j] = __uint_as_float(pack2<T>(w.x, w.y));
             }
-            tmem_st16(tS + 16 * c, pk);
+            tmem_st16(tP + 16 * c, pk);
           };
           if (whole) {
 #pragma unroll
@@ -428,12 +444,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           tc_fence_before();
           mbar_arrive(&pfull[sub]);
         }
-        if (ok && !wait(&odone[sub], oph)) {
+        if (ok && !wait(&pvdone[sub], vph)) {
           give_up();
           ok = false;
         }
         if (!ok) break;
-        oph ^= 1u;
+        vph ^= 1u;
         tc_fence_after();
       }
       // output rows; a row that sees nothing is zero.  A thread holds a row of O, so 32
@@ -498,7 +514,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const uint64_t dv0 = smem_desc_sw128(smem_u32(smem), 1024u, L::kGroupBytes);
       constexpr uint32_t kTile16 = L::kTileBytes / 16;
       // slot and phase of the next V tile (fill 1, 3, ..) and the next K tile (0, 2, ..)
-      uint32_t sk = 0, kph = 0, sv = 1, vph = 0, qph = 0, pph0 = 0, pph1 = 0;
+      uint32_t sk = 0, kph = 0, sv = 1, vph = 0, qph = 0, pph0 = 0, pph1 = 0, fph0 = 0, fph1 = 0;
       auto next = [](uint32_t& sl, uint32_t& ph) {  // two fills on
         sl += 2;
         if (sl >= (uint32_t)L::kSlots) {
@@ -513,7 +529,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = (ks & 3) * 32;
-          tc_mma_f16(tbase + (uint32_t)(j * 128),
+          tc_mma_f16(tbase,
                      dq0 + ((j * L::kSubBytes + (ks >> 2) * (kPfSub * 128) + off) >> 4),
                      dk + (((ks >> 2) * 1024 + off) >> 4), idesc_qk, ks > 0);
         }
@@ -525,8 +541,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (!one) return;
 #pragma unroll
         for (int kk = 0; kk < kPfKeys / 16; ++kk)
-          tc_mma_f16_ts(tbase + kOCols + (uint32_t)(j * 128), tbase + (uint32_t)(j * 128 + kk * 8),
+          tc_mma_f16_ts(tbase + kOCols + (uint32_t)(j * 128),
+                        tbase + kPCols + (uint32_t)(j * 64 + kk * 8),
                         dv + ((kk * 2 * L::kGroupBytes) >> 4), idesc_pv, more || kk > 0);
+        tc_commit(&pvdone[j]);
       };
       // (votes and reductions, so that the compiler sees one value for the warp)
       auto got = [](bool x) { return (bool)__all_sync(0xffffffffu, x); };
@@ -538,42 +556,56 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int tiles = __reduce_max_sync(0xffffffffu, it.tiles);
         const bool two = __any_sync(0xffffffffu, it.ntok > pf_tokens(group));
         if (tiles > 0) {
+          // Q K^T of subtile j may overwrite S when the softmax has taken the last scores that
+          // were put there (the other subtile's, or its own when there is one only)
+          auto s_free = [&](int j, uint32_t& ph) {
+            const bool x = got(wait(&sfree[j], ph));
+            ph ^= 1u;
+            return x;
+          };
           ok = got(wait(qfull, qph)) && got(wait(&kvfull[sk], kph));
           qph ^= 1u;
           if (ok) {
             tc_fence_after();
             qk(A);
-            if (two) qk(B);
+            if (two) {
+              ok = s_free(0, fph0);
+              tc_fence_after();
+              if (ok) qk(B);
+            }
             if (one) tc_commit(&kvempty[sk]);
             if (tiles == 1 && one) tc_commit(qempty);
             next(sk, kph);
           }
           for (int i = 0; ok && i < tiles; ++i) {
             const bool more = i + 1 < tiles;
-            ok = got(wait(&kvfull[sv], vph)) && got(wait(&pfull[0], pph0));
+            ok = two ? s_free(1, fph1) : s_free(0, fph0);
             if (!ok) break;
-            pph0 ^= 1u;
-            tc_fence_after();
-            pv(A, i > 0);
-            if (!more && one) tc_commit(&odone[0]);
             if (more) {
               ok = got(wait(&kvfull[sk], kph));
               if (!ok) break;
               tc_fence_after();
               qk(A);
             }
+            ok = got(wait(&kvfull[sv], vph)) && got(wait(&pfull[0], pph0));
+            if (!ok) break;
+            pph0 ^= 1u;
+            tc_fence_after();
+            pv(A, i > 0);
             if (two) {
+              if (more) {
+                ok = s_free(0, fph0);
+                if (!ok) break;
+                tc_fence_after();
+                qk(B);
+              }
               ok = got(wait(&pfull[1], pph1));
               if (!ok) break;
               pph1 ^= 1u;
               tc_fence_after();
               pv(B, i > 0);
-              if (!more && one) tc_commit(&odone[1]);
-              if (one) tc_commit(&kvempty[sv]);
-              if (more) qk(B);
-            } else {
-              if (one) tc_commit(&kvempty[sv]);
             }
+            if (one) tc_commit(&kvempty[sv]);
             next(sv, vph);
             if (more) {
               if (one) tc_commit(&kvempty[sk]);
