@@ -71,6 +71,8 @@ int wide_min_cols() {
   return v;
 }
 
+constexpr int kWindowMinUnits = 12, kWindowMaxSplit = 12;   // see decode_impl
+
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -261,6 +263,20 @@ pa_status decode_impl(void* out, const void* q, const void* k_cache, const void*
   const int cap = grid_cap > 0 ? (wide ? grid_cap / pkv::kMaxCtasPerSm : grid_cap) : 0;
   if (cap > 0 && grid > cap) grid = cap;
   if (cx.max_grid > 0 && grid > cx.max_grid) grid = cx.max_grid;
+  if (cx.mode == pkv::kWindow) {
+    // What a window leaves of a sequence is short and bounded, so few sequences are not cut
+    // over all CTAs: a CTA gets at least kWindowMinUnits units, a segment at most
+    // kWindowMaxSplit CTAs, since their partials meet in one CTA at the end (one sequence,
+    // 32/8 heads, window 1024: 14.1 us against 32 over all CTAs; window 4096: 21.0 against
+    // 37; 12 to 16 units and 8 to 16 CTAs are within 2 us of each other there)
+    const long long cap = (long long)max_blocks_per_seq * block_size;
+    const long long tokens = std::min(
+        cap, (long long)cx.window + q_len + 2 * pkv::kUnit + std::min<long long>(cx.num_sinks, cap));
+    const long long segs = (long long)num_seqs * num_kv_heads;
+    const long long units = segs * ((tokens + pkv::kUnit - 1) / pkv::kUnit);
+    grid = (int)std::max<long long>(
+        1, std::min({(long long)grid, units / kWindowMinUnits, segs * kWindowMaxSplit}));
+  }
   const WsLayout w = ws_layout(head_dim, grid, wide ? pkv::kWideCols : pkv::kMaxGroup);
   if (workspace_bytes < w.total) return PA_ERR_INVALID;
 

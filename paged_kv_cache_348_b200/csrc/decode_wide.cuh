@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
     // Event driven: QK^T of a stage is issued as soon as its tiles have landed and its
     // slot's S^T buffer is free (at most kWideStages stages ahead of PV), PV as soon as the
     // softmax has written P^T.
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc_qk = idesc_f16(kAB, 0u, 0u, 128u, (uint32_t)NC);
       const uint32_t idesc_pv = idesc_f16(kAB, 1u, 1u, (uint32_t)D, (uint32_t)kNPV);
       // descriptors of slot 0; slots, k-steps and column halves add to the start-address
@@ -1013,20 +1013,7 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
           named_bar_sync(1, kWideSoftThreads);
           const SplitDesc dsc = desc[mt.qslot];
           if (tid == 0) {
-            unsigned long long* ctr = a.counters + dsc.cf;
-            unsigned long long old =
-                dsc.cf == c ? ((unsigned long long)a.epoch << 32) | (uint32_t)(dsc.ncontrib - 1) : 0ull,
-                nxt;
-            for (;;) {
-              nxt = (uint32_t)(old >> 32) == a.epoch ? old + 1
-                                                      : ((unsigned long long)a.epoch << 32) | 1ull;
-              const unsigned long long prev = cas_acq_rel_gpu(ctr, old, nxt);
-              if (prev == old) break;
-              old = prev;
-            }
-            const bool last = (int)(uint32_t)nxt == dsc.ncontrib;
-            if (last) st_relaxed_gpu(ctr, 0ull);
-            *last_flag = last;
+            *last_flag = arrive_last(a.counters + dsc.cf, a.epoch, dsc.ncontrib, dsc.cf == c);
           }
           named_bar_sync(1, kWideSoftThreads);
           if (*last_flag) merge_wide<T, D, MODE, kWideSoftThreads>(a, dsc, *total_s, G, tid);
