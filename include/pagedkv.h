@@ -611,7 +611,8 @@ pa_status pa_bm_append_tokens(pa_block_manager* bm, const int32_t* seqs, int n, 
  * to the back of the free queue. */
 pa_status pa_bm_release(pa_block_manager* bm, int32_t seq);
 
-/* Cached tokens / blocks held by a sequence (-1: unknown sequence). */
+/* Cached tokens / blocks held by a sequence (-1: unknown sequence); without the pages that
+ * pa_bm_drop_window gave back. */
 int64_t pa_bm_context_len(const pa_block_manager* bm, int32_t seq);
 int pa_bm_num_blocks_of(const pa_block_manager* bm, int32_t seq);
 
@@ -650,6 +651,39 @@ pa_status pa_bm_slot_of(const pa_block_manager* bm, int32_t seq, int64_t pos, in
  */
 pa_status pa_bm_swap_out(pa_block_manager* bm, int32_t seq, int32_t* blocks, int* num_blocks);
 pa_status pa_bm_swap_in(pa_block_manager* bm, int32_t seq, int32_t* blocks, int* num_blocks);
+
+/*
+ * Bounded caches: giving pages of a live sequence back.
+ *
+ * Defined by [P2] "Core Principle" (blocks return to the pool when they are no longer needed)
+ * and [P1] "Why KV cache memory was the bottleneck".
+ *
+ * pa_bm_drop_window -- the pages of seq that hold only positions t with num_sinks <= t <
+ * len - window, which no token at position len - 1 or later sees with that window and that
+ * many first tokens (pa_decode_window, pa_prefill_window).  Each goes back as pa_bm_release
+ * would give it back (a shared block stays with its other sequences) and its table entry
+ * becomes -1; *num_dropped counts them.  The length does not change, and appending goes on as
+ * before.  pa_bm_num_blocks_of counts the pages still held, pa_bm_max_blocks the entries;
+ * pa_bm_slot_of refuses a position whose page is gone, pa_bm_plan_cascade and pa_plan_cascade
+ * a table with such an entry; a fork shares what is left, and swapping out and in keeps the
+ * entries that are gone gone.  PA_ERR_INVALID for an unknown or swapped-out sequence, window
+ * < 1 or num_sinks < 0.
+ *
+ * pa_bm_compact -- the tables of seqs[0..n) after pa_compact_tokens: sequence i keeps
+ * new_lens[i] <= its length tokens, in pages 0, 1, ... of a new table.  Entry j of the new
+ * table is entry j of the old one where seq alone holds that block, else (a shared block, or a
+ * page that is gone) a fresh one; every other block is given back.  tables[n][width] (HOST)
+ * gets the new tables (entries past a table's end = fill): the destination tables of
+ * pa_compact_tokens, whose source tables and context_lens are the ones from before this call
+ * (pa_bm_block_tables).  Enqueue pa_compact_tokens before anything else writes into the pool.
+ * From then on positions are those of the compacted cache.  PA_ERR_INVALID (nothing changed)
+ * for an unknown, swapped-out or repeated sequence, a length out of range or a table wider than
+ * width; PA_ERR_NO_BLOCKS (nothing changed) when the fresh blocks are not there.
+ */
+pa_status pa_bm_drop_window(pa_block_manager* bm, int32_t seq, int window, int num_sinks,
+                            int* num_dropped);
+pa_status pa_bm_compact(pa_block_manager* bm, const int32_t* seqs, const int32_t* new_lens, int n,
+                        int width, int32_t fill, int32_t* tables);
 
 /*
  * Cascade planning: the inputs pa_decode_cascade takes (prefix_lens, chunk_members,

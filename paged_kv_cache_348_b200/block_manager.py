@@ -70,6 +70,10 @@ def _lib():
         L.pa_bm_swap_out.restype = i32
         L.pa_bm_swap_in.argtypes = [P, i32, P, P]
         L.pa_bm_swap_in.restype = i32
+        L.pa_bm_drop_window.argtypes = [P, i32, i32, i32, P]
+        L.pa_bm_drop_window.restype = i32
+        L.pa_bm_compact.argtypes = [P, P, P, i32, i32, i32, P]
+        L.pa_bm_compact.restype = i32
         L._bm_ready = True
     return L
 
@@ -213,9 +217,35 @@ class BlockManager:
                     "swap_in")
         return out[:k.value].copy()
 
+    def drop_window(self, sid: int, window: int, num_sinks: int = 0) -> int:
+        """Give back the pages of `sid` that lie wholly behind a sliding window and past the
+        first num_sinks tokens (pa_bm_drop_window); their table entries become -1.  Returns
+        how many."""
+        k = ctypes.c_int()
+        self._check(self._L.pa_bm_drop_window(self._h, int(sid), pk._whole(window, "window"),
+                                              pk._whole(num_sinks, "num_sinks"),
+                                              ctypes.byref(k)), "drop_window")
+        return k.value
+
+    def compact(self, sids, new_lens, width: int | None = None, fill: int = 0) -> np.ndarray:
+        """The tables of sids after pa_compact_tokens leaves new_lens[i] tokens of sids[i]
+        (pa_bm_compact), int32 [n, width]: its destination tables.  Take the source tables
+        and lengths (block_tables, context_lens) before this call."""
+        s = np.ascontiguousarray(np.asarray(list(sids), dtype=np.int32))
+        n = np.ascontiguousarray(np.asarray(list(new_lens), dtype=np.int32))
+        if s.shape != n.shape:
+            raise ValueError("one new length per sequence")
+        if width is None:
+            width = max([1, *(-(-int(x) // self.block_size) for x in n)])
+        out = np.empty((len(s), int(width)), dtype=np.int32)
+        self._check(self._L.pa_bm_compact(self._h, _ptr(s), _ptr(n), len(s), int(width),
+                                          int(fill), _ptr(out)), "compact")
+        return out
+
     # ---------------------------------------------------------------- views
     def table(self, sid: int) -> list[int]:
-        n = int(self._L.pa_bm_num_blocks_of(self._h, int(sid)))
+        s = np.array([sid], dtype=np.int32)
+        n = int(self._L.pa_bm_max_blocks(self._h, _ptr(s), 1))
         if n < 0:
             raise KeyError(sid)
         return [int(x) for x in self.block_tables([sid], width=max(n, 1))[0, :n]]

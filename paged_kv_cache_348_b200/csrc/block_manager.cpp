@@ -23,6 +23,7 @@
 #include <deque>
 #include <new>
 #include <unordered_map>
+#include <unordered_set>
 #include <vector>
 
 #include "pagedkv.h"
@@ -32,6 +33,8 @@ struct pa_block_manager {
     std::vector<int32_t> table;  // logical block i -> physical block
     int64_t len = 0;             // cached tokens
     bool swapped = false;        // preempted: holds no block, keeps its length
+    int64_t holes = 0;           // table entries that are -1 (pages behind a window)
+    std::vector<uint8_t> hole;   // while swapped: which entries were
   };
   int32_t num_blocks = 0, block_size = 0;
   std::vector<int32_t> ref;      // reference count per physical block
@@ -122,7 +125,8 @@ pa_status pa_bm_fork(pa_block_manager* bm, int32_t seq, int32_t* child) {
   const pa_block_manager::Seq* p = bm->resident(seq);
   if (!p) return PA_ERR_INVALID;
   pa_block_manager::Seq c = *p;                  // shares every block of the parent
-  for (int32_t b : c.table) ++bm->ref[(size_t)b];
+  for (int32_t b : c.table)
+    if (b >= 0) ++bm->ref[(size_t)b];
   const int32_t id = bm->next_id++;
   bm->seqs.emplace(id, std::move(c));
   *child = id;
@@ -197,7 +201,8 @@ pa_status pa_bm_release(pa_block_manager* bm, int32_t seq) {
   if (!bm) return PA_ERR_INVALID;
   auto it = bm->seqs.find(seq);
   if (it == bm->seqs.end()) return PA_ERR_INVALID;
-  for (int32_t b : it->second.table) bm->drop(b);
+  for (int32_t b : it->second.table)
+    if (b >= 0) bm->drop(b);
   bm->seqs.erase(it);
   return PA_OK;
 }
@@ -209,7 +214,7 @@ int64_t pa_bm_context_len(const pa_block_manager* bm, int32_t seq) {
 
 int pa_bm_num_blocks_of(const pa_block_manager* bm, int32_t seq) {
   const pa_block_manager::Seq* s = bm ? bm->find(seq) : nullptr;
-  return s ? (int)s->table.size() : -1;
+  return s ? (int)((int64_t)s->table.size() - (s->swapped ? 0 : s->holes)) : -1;
 }
 
 int pa_bm_max_blocks(const pa_block_manager* bm, const int32_t* seqs, int n) {
@@ -244,7 +249,9 @@ pa_status pa_bm_block_tables(const pa_block_manager* bm, const int32_t* seqs, in
 pa_status pa_bm_slot_of(const pa_block_manager* bm, int32_t seq, int64_t pos, int64_t* slot) {
   const pa_block_manager::Seq* s = bm ? bm->resident(seq) : nullptr;
   if (!s || !slot || pos < 0 || pos >= s->len) return PA_ERR_INVALID;
-  *slot = (int64_t)s->table[(size_t)(pos / bm->block_size)] * bm->block_size + pos % bm->block_size;
+  const int32_t b = s->table[(size_t)(pos / bm->block_size)];
+  if (b < 0) return PA_ERR_INVALID;                // its page was given back
+  *slot = (int64_t)b * bm->block_size + pos % bm->block_size;
   return PA_OK;
 }
 
@@ -257,9 +264,20 @@ pa_status pa_bm_swap_out(pa_block_manager* bm, int32_t seq, int32_t* blocks, int
   if (!bm || !num_blocks) return PA_ERR_INVALID;
   pa_block_manager::Seq* s = bm->find(seq);
   if (!s || s->swapped || (!s->table.empty() && !blocks)) return PA_ERR_INVALID;
-  const size_t n = s->table.size();
-  if (n) std::memcpy(blocks, s->table.data(), n * sizeof(int32_t));
-  for (int32_t b : s->table) bm->drop(b);
+  if (s->holes) {
+    try {
+      s->hole.assign(s->table.size(), 0);
+    } catch (...) {
+      return PA_ERR_NO_MEMORY;
+    }
+  }
+  size_t n = 0;
+  for (size_t i = 0; i < s->table.size(); ++i) {
+    if (s->table[i] >= 0) blocks[n++] = s->table[i];
+    else s->hole[i] = 1;
+  }
+  for (int32_t b : s->table)
+    if (b >= 0) bm->drop(b);
   s->table.clear();
   s->swapped = true;
   *num_blocks = (int)n;
@@ -270,13 +288,86 @@ pa_status pa_bm_swap_in(pa_block_manager* bm, int32_t seq, int32_t* blocks, int*
   if (!bm || !num_blocks) return PA_ERR_INVALID;
   pa_block_manager::Seq* s = bm->find(seq);
   if (!s || !s->swapped) return PA_ERR_INVALID;
-  const int64_t need = bm->blocks_for(s->len);
+  const int64_t all = bm->blocks_for(s->len), need = all - s->holes;
   if (need && !blocks) return PA_ERR_INVALID;
   if (need > (int64_t)bm->free.size()) return PA_ERR_NO_BLOCKS;
-  s->table.resize((size_t)need);
-  for (int64_t i = 0; i < need; ++i) s->table[(size_t)i] = blocks[i] = bm->take();
+  s->table.resize((size_t)all);
+  int64_t k = 0;
+  for (int64_t i = 0; i < all; ++i)
+    s->table[(size_t)i] = s->holes && s->hole[(size_t)i] ? -1 : (blocks[k++] = bm->take());
+  s->hole.clear();
   s->swapped = false;
   *num_blocks = (int)need;
+  return PA_OK;
+}
+
+// Bounded caches ("Core Principle": blocks go back to the pool as soon as nothing needs them):
+// pages that lie wholly behind a sliding window and past the first tokens, and pages that a
+// compaction of the kept tokens empties.
+pa_status pa_bm_drop_window(pa_block_manager* bm, int32_t seq, int window, int num_sinks,
+                            int* num_dropped) {
+  if (!bm || !num_dropped || window < 1 || num_sinks < 0) return PA_ERR_INVALID;
+  pa_block_manager::Seq* s = bm->find(seq);
+  if (!s || s->swapped) return PA_ERR_INVALID;
+  const int64_t bs = bm->block_size, behind = s->len - window;   // positions < behind are
+  int n = 0;
+  for (int64_t i = (num_sinks + bs - 1) / bs; (i + 1) * bs <= behind; ++i) {
+    int32_t& b = s->table[(size_t)i];
+    if (b < 0) continue;
+    bm->drop(b);
+    b = -1;
+    ++s->holes;
+    ++n;
+  }
+  *num_dropped = n;
+  return PA_OK;
+}
+
+pa_status pa_bm_compact(pa_block_manager* bm, const int32_t* seqs, const int32_t* new_lens, int n,
+                        int width, int32_t fill, int32_t* tables) {
+  if (!bm || n < 0 || (n && (!seqs || !new_lens || !tables || width <= 0))) return PA_ERR_INVALID;
+  try {
+    // every sequence once, and what the batch needs: a new table keeps the entries that its
+    // sequence alone holds (counts as they are before the call, so that a block that two
+    // sequences of the batch share is a source for both and a destination for neither)
+    std::unordered_set<int32_t> once;
+    std::vector<std::vector<int32_t>> fresh((size_t)n);   // new tables, -1: a fresh block
+    int64_t need = 0;
+    for (int i = 0; i < n; ++i) {
+      const pa_block_manager::Seq* s = bm->resident(seqs[i]);
+      if (!s || new_lens[i] < 0 || new_lens[i] > s->len || !once.insert(seqs[i]).second)
+        return PA_ERR_INVALID;
+      const int64_t nb = bm->blocks_for(new_lens[i]);
+      if (nb > width) return PA_ERR_INVALID;
+      std::vector<int32_t>& t = fresh[(size_t)i];
+      t.resize((size_t)nb);
+      for (int64_t j = 0; j < nb; ++j) {
+        const int32_t b = s->table[(size_t)j];
+        const bool own = b >= 0 && bm->ref[(size_t)b] == 1;
+        t[(size_t)j] = own ? b : -1;
+        need += !own;
+      }
+    }
+    if (need > (int64_t)bm->free.size()) return PA_ERR_NO_BLOCKS;
+    // fresh blocks first, from the front of the queue; what is left over goes to its back
+    for (int i = 0; i < n; ++i)
+      for (int32_t& b : fresh[(size_t)i])
+        if (b < 0) b = bm->take();
+    for (int i = 0; i < n; ++i) {
+      pa_block_manager::Seq& s = *bm->find(seqs[i]);
+      std::vector<int32_t>& t = fresh[(size_t)i];
+      for (size_t j = 0; j < s.table.size(); ++j)
+        if (s.table[j] >= 0 && (j >= t.size() || t[j] != s.table[j])) bm->drop(s.table[j]);
+      int32_t* row = tables + (int64_t)i * width;
+      for (int j = 0; j < width; ++j) row[j] = j < (int)t.size() ? t[(size_t)j] : fill;
+      s.table.swap(t);
+      s.len = new_lens[i];
+      s.holes = 0;
+    }
+  } catch (...) {
+    return PA_ERR_NO_MEMORY;     // (only before the first change: nothing after it allocates
+                                 // but the free queue's tail)
+  }
   return PA_OK;
 }
 
@@ -378,6 +469,9 @@ pa_status pa_plan_cascade(const int32_t* block_tables, int max_blocks_per_seq,
   for (int i = 0; i < num_seqs; ++i) {     // every table must hold its sequence's blocks
     const int64_t c = context_lens[i];
     if (c < 0 || (c + block_size - 1) / block_size > max_blocks_per_seq) return PA_ERR_INVALID;
+    const int32_t* row = block_tables + (int64_t)i * max_blocks_per_seq;
+    for (int64_t j = 0; j < (c + block_size - 1) / block_size; ++j)
+      if (row[j] < 0) return PA_ERR_INVALID;       // a page that was given back
   }
   return plan_rows(
       num_seqs, block_size, group, chunk_width,
@@ -393,7 +487,7 @@ pa_status pa_bm_plan_cascade(const pa_block_manager* bm, const int32_t* seqs, in
   std::vector<const pa_block_manager::Seq*> rows((size_t)n);
   for (int i = 0; i < n; ++i) {
     rows[(size_t)i] = bm->resident(seqs[i]);
-    if (!rows[(size_t)i]) return PA_ERR_INVALID;
+    if (!rows[(size_t)i] || rows[(size_t)i]->holes) return PA_ERR_INVALID;
   }
   return plan_rows(
       n, bm->block_size, group, chunk_width,

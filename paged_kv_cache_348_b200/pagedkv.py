@@ -36,7 +36,7 @@ EXPORTS = ("pa_version", "pa_status_string", "pa_decode_workspace_bytes", "pa_de
            "pa_decode_e4m3_bs", "pa_decode_cascade_e4m3_bs", "pa_decode_append_e4m3_bs",
            "pa_check_bounded_waits", "pa_decode_window", "pa_decode_window_e4m3_bs",
            "pa_compact_tokens", "pa_compact_tokens_e4m3_bs", "pa_prefill_window",
-           "pa_prefill_workspace_bytes")
+           "pa_prefill_workspace_bytes", "pa_bm_drop_window", "pa_bm_compact")
 
 _lib = None
 _lock = threading.Lock()
