@@ -906,6 +906,7 @@ pa_status compact_args(pkv::CompactArgs& a, void* const* k_caches, void* const* 
   a.dst_width = dst_blocks_per_seq;
   a.num_kv_heads = num_kv_heads;
   a.block_size = block_size;
+  while ((1 << a.bs_log) < block_size) ++a.bs_log;
   a.num_blocks = num_blocks;
   a.max_keep = max_keep;
   a.keep_head = keep_per_head ? max_keep : 0;
