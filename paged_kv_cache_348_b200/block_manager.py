@@ -299,8 +299,13 @@ class BlockManager:
 
     def tail_waste(self, sids) -> float:
         """Fraction of held slots that hold no token: only the unused tail of each
-        sequence's last block (shared blocks counted once per sequence)."""
-        held = sum(int(self._L.pa_bm_num_blocks_of(self._h, int(s))) * self.block_size
-                   for s in sids)
-        used = sum(self.context_len(s) for s in sids)
+        sequence's last block (shared blocks counted once per sequence; tokens whose pages
+        drop_window gave back not counted)."""
+        held = used = 0
+        for sid in sids:
+            n = int(self._L.pa_bm_num_blocks_of(self._h, int(sid)))
+            s = np.array([sid], dtype=np.int32)
+            gone = int(self._L.pa_bm_max_blocks(self._h, _ptr(s), 1)) - n
+            held += n * self.block_size
+            used += self.context_len(sid) - gone * self.block_size
         return 0.0 if held == 0 else (held - used) / held

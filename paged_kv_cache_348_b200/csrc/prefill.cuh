@@ -277,8 +277,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (a.status) atomicOr(a.status, DEV_TIMEOUT);
     }
   };
+  // (a vote, so that a warp whose lanes disagree at the limit gives up as a whole: what follows
+  // a wait is done by whole warps)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_wait_bounded(bar, parity, abort_flag, kWaitLimitNs);
+    return (bool)__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, kWaitLimitNs));
   };
   // whether there is an item k of this CTA (false at the end of the launch or of patience);
   // its fields are read from its slot, which item_done hands back
@@ -545,24 +547,23 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         dv + ((kk * 2 * L::kGroupBytes) >> 4), idesc_pv, more || kk > 0);
         tc_commit(&pvdone[j]);
       };
-      // (votes and reductions, so that the compiler sees one value for the warp)
-      auto got = [](bool x) { return (bool)__all_sync(0xffffffffu, x); };
       std::integral_constant<int, 0> A;
       std::integral_constant<int, 1> B;
       bool ok = true;
-      for (int k = 0; ok && got(item_at(k)); ++k) {
+      for (int k = 0; ok && item_at(k); ++k) {
         const PfItem& it = items[k % kPfItems];
+        // (a reduction and a vote, so that the compiler sees one value for the warp)
         const int tiles = __reduce_max_sync(0xffffffffu, it.tiles);
         const bool two = __any_sync(0xffffffffu, it.ntok > pf_tokens(group));
         if (tiles > 0) {
           // Q K^T of subtile j may overwrite S when the softmax has taken the last scores that
           // were put there (the other subtile's, or its own when there is one only)
           auto s_free = [&](int j, uint32_t& ph) {
-            const bool x = got(wait(&sfree[j], ph));
+            const bool x = wait(&sfree[j], ph);
             ph ^= 1u;
             return x;
           };
-          ok = got(wait(qfull, qph)) && got(wait(&kvfull[sk], kph));
+          ok = wait(qfull, qph) && wait(&kvfull[sk], kph);
           qph ^= 1u;
           if (ok) {
             tc_fence_after();
@@ -581,12 +582,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             ok = two ? s_free(1, fph1) : s_free(0, fph0);
             if (!ok) break;
             if (more) {
-              ok = got(wait(&kvfull[sk], kph));
+              ok = wait(&kvfull[sk], kph);
               if (!ok) break;
               tc_fence_after();
               qk(A);
             }
-            ok = got(wait(&kvfull[sv], vph)) && got(wait(&pfull[0], pph0));
+            ok = wait(&kvfull[sv], vph) && wait(&pfull[0], pph0);
             if (!ok) break;
             pph0 ^= 1u;
             tc_fence_after();
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 tc_fence_after();
                 qk(B);
               }
-              ok = got(wait(&pfull[1], pph1));
+              ok = wait(&pfull[1], pph1);
               if (!ok) break;
               pph1 ^= 1u;
               tc_fence_after();

@@ -194,3 +194,11 @@ def test_tables_with_pages_gone_are_refused_where_they_cannot_work():
     with pytest.raises(ValueError):
         plan_cascade_tables(m.block_tables([a, b]), m.context_lens([a, b]), 4, 4)
     m.plan_cascade([b], 4)
+
+
+def test_tail_waste_counts_held_pages_only():
+    m = BlockManager(40, 4)
+    a = m.allocate(38)
+    assert m.tail_waste([a]) == 2 / 40
+    m.drop_window(a, 6, 0)                        # 32 positions and their pages gone
+    assert m.tail_waste([a]) == 2 / 8

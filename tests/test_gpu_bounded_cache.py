@@ -195,3 +195,72 @@ def test_compacting_forks_together_over_8_bit_pages():
         want, bound = ref.attend(q[i:i + 1].double(), k, v, torch.tensor([len(x) - 1]), 20, 2,
                                  D ** -0.5, 2.0 ** -11, "f16")
         ref.check(out[i:i + 1], want, bound)
+
+
+def test_two_calls_at_once():
+    """Prompt attention, windowed decode and a compaction on two streams at a time, a workspace
+    each: the results that they give alone."""
+    from tests.helpers import bits, from_bits, make_case
+
+    ctx = [3000, 900, 64, 1, 2222, 17]
+    case = make_case(6, 32, 8, 128, 16, ctx, dtype="bf16", seed=3, poison=False)
+    k, v = (from_bits(case[x], "bf16").cuda() for x in ("k", "v"))
+    tab, cl = torch.from_numpy(case["tables"]).cuda(), torch.from_numpy(case["ctx"]).cuda()
+    n = [1500, 900, 1, 1, 700, 5]
+    starts = torch.from_numpy(np.concatenate([[0], np.cumsum(n)]).astype(np.int32)).cuda()
+    q = from_bits(bits(inputs.randn((sum(n), 32, 128), "bf16", 1, stream=1)), "bf16").cuda()
+    qd = from_bits(bits(inputs.randn((6, 32, 128), "bf16", 1, stream=2)), "bf16").cuda()
+
+    def prefill(ws, stream=None):
+        out = torch.empty_like(q)
+        pk.pa_prefill_window(out, q, k, v, tab, cl, starts, 500, 4, 0.09, ws, None, stream)
+        return out
+
+    def decode(ws, stream=None):
+        out = torch.empty_like(qd)
+        pk.pa_decode_window(out, qd, k, v, tab, cl, 500, 4, 0.09, ws, None, stream)
+        return out
+
+    want = prefill(pk.new_prefill_workspace()), decode(pk.new_workspace(6, 32, 8, 128))
+    st = [torch.cuda.Stream() for _ in range(3)]
+    pws = [pk.new_prefill_workspace() for _ in range(2)]
+    dws = pk.new_workspace(6, 32, 8, 128)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = prefill(pws[0], st[0]), prefill(pws[1], st[1]), decode(dws, st[2])
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[0])
+        assert torch.equal(got[2], want[1])
+
+
+def test_offsets_past_32_bits():
+    """Pages at the end of a 6.4 GB pool (K and V one tensor) and the same pages in a small one:
+    the same bits from every operator."""
+    bs, Hkv, D, big = 16, 8, 128, 200_000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ctx = torch.tensor([1000, 333], dtype=torch.int32, device="cuda")
+    nb = [63, 21]
+    pool = torch.empty((big, Hkv, bs, D), dtype=torch.bfloat16, device="cuda")
+    small = torch.randn((90, Hkv, bs, D), generator=g, device="cuda").bfloat16()
+    pool[-90:] = small
+    tab = torch.zeros((2, 63), dtype=torch.int32, device="cuda")
+    tab[0] = torch.randperm(90, generator=g, device="cuda")[:63].int()
+    rest = torch.tensor(sorted(set(range(90)) - set(tab[0].tolist())), device="cuda").int()
+    tab[1, :21] = rest[:21]
+    starts = torch.tensor([0, 500, 520], dtype=torch.int32, device="cuda")
+    q = torch.randn((520, 16, D), generator=g, device="cuda").bfloat16()
+    qd = torch.randn((2, 16, D), generator=g, device="cuda").bfloat16()
+    keep = torch.arange(3, 203, dtype=torch.int32, device="cuda").view(1, 1, 1, 200).expand(
+        1, 2, 1, 200).contiguous()
+    n = torch.tensor([200, 150], dtype=torch.int32, device="cuda")
+    res = []
+    for p, off in ((small, 0), (pool, big - 90)):
+        t = (tab + off).contiguous()
+        a, b = torch.empty_like(q), torch.empty_like(qd)
+        pk.pa_prefill_window(a, q, p, p, t, ctx, starts, 300, 4, 0.09, pk.new_prefill_workspace())
+        pk.pa_decode_window(b, qd, p, p, t, ctx, 300, 4, 0.09, pk.new_workspace(2, 16, Hkv, D))
+        k2 = p if off else p.clone()
+        pk.pa_compact_tokens([k2], [torch.zeros_like(k2)], t, t[:, :13].contiguous(), ctx, keep, n)
+        res.append((a, b, k2[off:off + 90].clone() if off else k2))
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
