@@ -49,6 +49,8 @@ class PagedKVError(RuntimeError):
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -153,6 +155,9 @@ def _stream(stream):
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, ndim=None):
+    if t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype == dtype) and \
+            (ndim is None or t.dim() == ndim):
+        return
     if not t.is_cuda:
         raise PagedKVError("%s must be a CUDA tensor" % name)
     if not t.is_contiguous():
@@ -642,12 +647,13 @@ def _pool_args(k_caches, v_caches):
     if L != len(v_caches) or L == 0:
         raise PagedKVError("need the same non-zero number of K and V pools")
     shape, dt = k_caches[0].shape, k_caches[0].dtype
-    for i, c in enumerate(list(k_caches) + list(v_caches)):
-        _need(c, "cache[%d]" % i, dtype=dt, ndim=4)
-        if c.shape != shape:
-            raise PagedKVError("all pools must have one shape")
-    kp = (ctypes.c_void_p * L)(*[c.data_ptr() for c in k_caches])
-    vp = (ctypes.c_void_p * L)(*[c.data_ptr() for c in v_caches])
+    for pools, what in ((k_caches, "k_caches"), (v_caches, "v_caches")):
+        for c in pools:
+            _need(c, what, dtype=dt, ndim=4)
+            if c.shape != shape:
+                raise PagedKVError("all pools must have one shape")
+    P = ctypes.c_void_p * L
+    kp, vp = P(*[c.data_ptr() for c in k_caches]), P(*[c.data_ptr() for c in v_caches])
     block_bytes = shape[1] * shape[2] * shape[3] * k_caches[0].element_size()
     return L, kp, vp, shape[0], block_bytes
 
