@@ -124,30 +124,37 @@ __device__ __forceinline__ uint32_t below32(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
-// Hands out the items of a launch in order, whole warps at a time: sequences in batch order,
-// a sequence's row tiles from its last (longest) to its first, the kv heads of a row tile
-// side by side (their CTAs read the same block-table entries).
+// Hands out the items of a launch in order, whole warps at a time: the sequences with at least
+// one whole item of new tokens in batch order, then the others, whose items are short (a long
+// item drawn last is what a launch waits for: 24 ragged chunks 48.2 us against 49.6 in batch
+// order alone).  A sequence's items go from its last tokens
+// (most positions) to its first, the kv heads of an item's tokens side by side (their CTAs
+// read the same block-table entries).
 struct PfCursor {
+  bool rest = false;             // the sequences with fewer new tokens than an item holds
   long long base = 0;            // first item of the 32 sequences from sbase on
   int sbase = -32;
   long long incl = 0, sum = 0;   // this lane's inclusive item count, all lanes'
   int q0 = 0, n = 0, tiles = 0, ctx = 0;
 
   __device__ __forceinline__ void load(const PrefillArgs& a, int lane) {
-    const int s = sbase + lane;
-    q0 = n = tiles = ctx = 0;
-    if (s < a.num_seqs) {
-      ctx = clamp_ctx(a.context_lens[s], a.ctx_cap, a.status);
-      int b = a.q_starts[s], e = a.q_starts[s + 1];
-      if (b < 0 || e < b || e > a.total_q) {
-        if (a.status) atomicOr(a.status, DEV_BAD_QUERY);
-        b = e = 0;
+    // (one warp's worth of sequences is still here in the second round)
+    if (!rest || a.num_seqs > 32) {
+      const int s = sbase + lane;
+      q0 = n = ctx = 0;
+      if (s < a.num_seqs) {
+        ctx = clamp_ctx(a.context_lens[s], a.ctx_cap, a.status);
+        int b = a.q_starts[s], e = a.q_starts[s + 1];
+        if (b < 0 || e < b || e > a.total_q) {
+          if (a.status) atomicOr(a.status, DEV_BAD_QUERY);
+          b = e = 0;
+        }
+        q0 = b;
+        n = e - b;
       }
-      q0 = b;
-      n = e - b;
-      const int per = 2 * pf_tokens(a.group);
-      tiles = (n + per - 1) / per;
     }
+    const int per = 2 * pf_tokens(a.group);
+    tiles = (n < per) == rest ? (n + per - 1) / per : 0;
     incl = (long long)tiles * a.num_kv_heads;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -163,9 +170,13 @@ struct PfCursor {
       if (sbase >= 0) base += sum;
       sbase += 32;
       if (sbase >= a.num_seqs) {
-        it.end = 1;
-        sum = 0;
-        return it;
+        if (rest) {
+          it.end = 1;
+          sum = 0;
+          return it;
+        }
+        rest = true;
+        sbase = 0;
       }
       load(a, lane);
     }
