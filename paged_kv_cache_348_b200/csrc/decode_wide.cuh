@@ -956,10 +956,8 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
         const int d = D == 128 ? r : (lane < 16 ? q4 * 16 + lane : -1);
         const bool complete = mt.flags & F_COMPLETE;
         const float* mc = mref + cur * kWideCols;
-        // O^T back 8 columns at a time (the high part plus, with bf16, the residual part)
-#pragma unroll 1
-        for (int j0 = 0; j0 < CW; j0 += 8) {
-          float o[8];
+        // 8 columns of O^T back (the high part plus, with bf16, the residual part)
+        auto columns = [&](int j0, float* o) {
           tmem_ld8(trow_addr + kOCol + (uint32_t)(c0 + j0), o);
           if constexpr (kSplit) {
             float o2[8];
@@ -970,41 +968,56 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
           } else {
             tmem_wait_ld();
           }
+        };
+        auto sum_of = [&](int cq) {
+          const float4 w4 = *reinterpret_cast<const float4*>(red + cq * 4);
+          return (w4.x + w4.y) + (w4.z + w4.w);
+        };
+        // the two ways out in loops of their own: this code runs once a portion, from a cold
+        // instruction cache, so its length is what it costs (4 new tokens of the 70B shape 102.5
+        // -> 100.5 us, with a window of 1001 48.4 -> 45.1, 8 new tokens 73.0 -> 67.3)
+        if (complete) {
+#pragma unroll 1
+          for (int j0 = 0; j0 < CW; j0 += 8) {
+            float o[8];
+            columns(j0, o);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int cq = c0 + j0 + j;
-            if (cq < a.ncol && d >= 0) {
-              const float4 w4 = *reinterpret_cast<const float4*>(red + cq * 4);
-              const float Ls = (w4.x + w4.y) + (w4.z + w4.w);
-              const float M = mc[cq];
-              if (complete) {
+            for (int j = 0; j < 8; ++j) {
+              const int cq = c0 + j0 + j;
+              if (cq < a.ncol && d >= 0) {
+                const float Ls = sum_of(cq);
                 // output row of column cq: out_row without its divisions
-                long long row;
                 if constexpr (MODE == kPrefix) {
                   const int mem = chunk_member(a, mt.seq, colj[cq]);
-                  row = mem < 0 ? -1ll
-                                : (long long)mem * a.num_q_heads + (long long)mt.kvh * group + colg[cq];
-                } else {
-                  row = ((long long)mt.seq * a.q_len + colj[cq]) * a.num_q_heads +
-                        (long long)mt.kvh * group + colg[cq];
-                }
-                if (row >= 0) {
-                  if constexpr (MODE == kPrefix) {
-                    if (d == 0) a.ext_ml[row] = make_float2(M, Ls);
+                  const long long row = mem < 0 ? -1ll
+                                                : (long long)mem * a.num_q_heads +
+                                                      (long long)mt.kvh * group + colg[cq];
+                  if (row >= 0) {
+                    if (d == 0) a.ext_ml[row] = make_float2(mc[cq], Ls);
                     a.ext_acc[row * D + d] = o[j];
-                  } else {
-                    static_cast<T*>(a.out)[row * D + d] = from_float<T>(Ls > 0.f ? o[j] / Ls : 0.f);
                   }
-                }
-              } else {
-                const long long prow = (long long)mt.pidx * kWideCols + cq;
-                a.part_acc[prow * D + d] = o[j];
-                if (d == 0) {
-                  a.part_ml[prow * 2 + 0] = M;
-                  a.part_ml[prow * 2 + 1] = Ls;
+                } else {
+                  const long long row = ((long long)mt.seq * a.q_len + colj[cq]) * a.num_q_heads +
+                                        (long long)mt.kvh * group + colg[cq];
+                  static_cast<T*>(a.out)[row * D + d] = from_float<T>(Ls > 0.f ? o[j] / Ls : 0.f);
                 }
               }
             }
+          }
+        } else {
+#pragma unroll 1
+          for (int j0 = 0; j0 < CW; j0 += 8) {
+            float o[8];
+            columns(j0, o);
+            const long long prow = (long long)mt.pidx * kWideCols + c0 + j0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (c0 + j0 + j < a.ncol && d >= 0) a.part_acc[(prow + j) * D + d] = o[j];
+          }
+          if (r < CW && c0 + r < a.ncol) {            // one thread a column
+            const long long prow = (long long)mt.pidx * kWideCols + c0 + r;
+            a.part_ml[prow * 2 + 0] = mc[c0 + r];
+            a.part_ml[prow * 2 + 1] = sum_of(c0 + r);
           }
         }
         tc_fence_before();
