@@ -1587,14 +1587,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
         xv[it] = (MODE == kSuffix && has_prefix && crow[n] >= 0) ? __ldcg(a.ext_acc + crow[n] * D + d)
                                                                   : 0.f;
       }
-#pragma unroll
-      for (int it = 0; it < kIt; ++it) {
+      // accumulator value `it` of this thread, summed over the warps holding its n-tile
+      auto value = [&](int it) {
         const int n = it % NT, ks = it / NT;
-        const int h = n * 8 + 2 * (lane & 3) + (cw & 1);   // query column
-        if (h >= a.ncol) continue;
-        // head dim of this accumulator value (8-bit caches order the PV rows 2g, 2g+1)
-        const int d = ks * 16 + (KV8 ? 2 * (lane >> 2) + (cw >= 2 ? 1 : 0)
-                                     : (lane >> 2) + (cw >= 2 ? 8 : 0));
         float acc = 0.f;
 #pragma unroll
         for (int w = 0; w < kConsumerWarps; ++w) {
@@ -1602,13 +1597,30 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
           if (nl >= 0 && nl < NTW)
             acc += scr[(w * NREGW + (ks * NTW + nl) * 4 + cw) * 32 + lane] * cs[n][w];
         }
-        if (complete) {
+        return acc;
+      };
+      // its head dim (8-bit caches order the PV rows 2g, 2g+1)
+      auto dim = [&](int it) {
+        return it / NT * 16 + (KV8 ? 2 * (lane >> 2) + (cw >= 2 ? 1 : 0)
+                                   : (lane >> 2) + (cw >= 2 ? 8 : 0));
+      };
+      if (complete) {
+#pragma unroll
+        for (int it = 0; it < kIt; ++it) {
+          const int n = it % NT, h = n * 8 + 2 * (lane & 3) + (cw & 1);   // query column
+          if (h >= a.ncol || crow[n] < 0) continue;
+          float acc = value(it);
           // column h = new token (or chunk member) h / group, head kvh * group + h % group;
           // a row that sees no token at all (a new token before the context start) is zero
-          if (crow[n] >= 0)
-            finish_row<T, MODE, D>(a, crow[n], cM[n], cL[n], &acc, d, 1, xm[n], &xv[it]);
-        } else {
-          a.part_acc[((long long)mt.pidx * kMaxGroup + h) * D + d] = acc;
+          finish_row<T, MODE, D>(a, crow[n], cM[n], cL[n], &acc, dim(it), 1, xm[n], &xv[it]);
+        }
+      } else {
+#pragma unroll
+        for (int it = 0; it < kIt; ++it) {
+          const int n = it % NT, h = n * 8 + 2 * (lane & 3) + (cw & 1);
+          if (h >= a.ncol) continue;
+          const int d = dim(it);
+          a.part_acc[((long long)mt.pidx * kMaxGroup + h) * D + d] = value(it);
           if (d == 0) {
             a.part_ml[((long long)mt.pidx * kMaxGroup + h) * 2 + 0] = cM[n];
             a.part_ml[((long long)mt.pidx * kMaxGroup + h) * 2 + 1] = cL[n];
