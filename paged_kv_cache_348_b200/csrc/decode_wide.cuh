@@ -633,7 +633,10 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
     // slot's S^T buffer is free (at most kWideStages stages ahead of PV), PV as soon as the
     // softmax has written P^T.
     if (elect_one()) {
-      const uint32_t idesc_qk = idesc_f16(kAB, 0u, 0u, 128u, (uint32_t)NC);
+      // a negative scale: -K in its place and the scale's magnitude below, so that a masked
+      // score's -inf stays the smallest
+      const uint32_t idesc_qk = idesc_f16(kAB, 0u, 0u, 128u, (uint32_t)NC) |
+                                (a.scale_log2 < 0.f ? kIdescNegateA : 0u);
       const uint32_t idesc_pv = idesc_f16(kAB, 1u, 1u, (uint32_t)D, (uint32_t)kNPV);
       // descriptors of slot 0; slots, k-steps and column halves add to the start-address
       // field (16-byte units, bits 0..13; every address here is below 256 KB, so the sum
@@ -812,7 +815,7 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
       // reference maxima in force: a portion's first stage starts from the -inf row.  With
       // x = scale * s (base 2), e = max_j (x_j - m_j) tells whether a reference must move;
       // masked scores are -inf (NaN against a -inf reference, which fmaxf ignores)
-      const float sc = a.scale_log2;
+      const float sc = fabsf(a.scale_log2);
       const float* mcur = mref + (first ? 2 : cur) * kWideCols;
       float e = -INFINITY;
       if (tv && (MODE == kPrefix || r < lim0) && (MODE != kWindow || wend >= a.q_len)) {

@@ -138,7 +138,7 @@ struct PfCursor {
   int q0 = 0, n = 0, tiles = 0, ctx = 0;
 
   __device__ __forceinline__ void load(const PrefillArgs& a, int lane) {
-    // (one warp's worth of sequences is still here in the second round)
+    // (one warp's worth of sequences is still here in the second pass)
     if (!rest || a.num_seqs > 32) {
       const int s = sbase + lane;
       q0 = n = ctx = 0;

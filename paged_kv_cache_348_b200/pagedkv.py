@@ -8,6 +8,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 
@@ -495,9 +496,10 @@ def _here(what, *tensors):
 
 def _whole(x, name: str) -> int:
     """A whole number as the C int it becomes, saturated at the largest one."""
-    if not isinstance(x, int):
-        raise PagedKVError("%s must be an int" % name)
-    return max(-1, min(x, 0x7fffffff))
+    try:
+        return max(-1, min(operator.index(x), 0x7fffffff))
+    except TypeError:
+        raise PagedKVError("%s must be an int" % name) from None
 
 
 def _window_shapes(what, out, q, k_cache, v_cache, block_tables, context_lens, workspace):

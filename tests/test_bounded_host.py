@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import ctypes
 
+import numpy as np
 import pytest
 
 from paged_kv_cache_348_b200 import build as pbuild
@@ -85,4 +86,5 @@ def test_wrappers_refuse_what_is_not_an_int():
     for bad in (1.0, "8", None):
         with pytest.raises(pk.PagedKVError):
             pk._whole(bad, "window")
+    assert pk._whole(np.int64(5), "window") == 5
     assert pk._whole(1 << 60, "window") == 0x7fffffff and pk._whole(-(1 << 60), "w") == -1

@@ -159,6 +159,57 @@ def test_captured_on_another_stream_and_two_graphs_of_one_workspace():
         assert torch.equal(got, want)
 
 
+def test_captured_with_more_items_than_ctas():
+    """CTAs that draw items from the workspace's counter, replayed: two graphs in turn on one
+    workspace, behind a decode whose launch they overlap, then new chunk lengths."""
+    mix = [(1500, 1600), (3, 64), (700, 700), (0, 9), (64, 1000)]
+    case, starts, q = setup(mix, 32, 8, 128, 16, "bf16", 150, 4, 4, drop=False)
+    want, st = run(case, starts, q, 150, 4)
+    assert st == 0
+    ref.check(want, *expect(case, starts, q, 150, 4))
+    dev = [from_bits(x, "bf16").cuda() for x in (q, case["k"], case["v"])]
+    tab, cl = torch.from_numpy(case["tables"]).cuda(), torch.from_numpy(case["ctx"]).cuda()
+    sd = torch.from_numpy(starts).cuda()
+    ws, dws = pk.new_prefill_workspace(), pk.new_workspace(5, 32, 8, 128)
+    got = torch.full_like(want, 7.0)
+    dq = torch.randn((5, 32, 128), device="cuda").bfloat16()
+    dout = torch.empty_like(dq)
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:
+        with torch.cuda.graph(g):
+            pk.pa_decode_window(dout, dq, dev[1], dev[2], tab, cl, 150, 4, case["scale"], dws)
+            pk.pa_prefill_window(got, *dev, tab, cl, sd, 150, 4, case["scale"], ws)
+            pk.pa_prefill_window(got, *dev, tab, cl, sd, 150, 4, case["scale"], ws)
+    for g in graphs + graphs[::-1]:
+        got.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    late = np.array([0, 100, 1400, 1400, 1409, 1409], np.int32)     # other chunks, same graph
+    sd.copy_(torch.from_numpy(late))
+    got.fill_(7.0)
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    again, st = run(case, late, q, 150, 4)
+    # (sequence 3 had no new tokens before, so its rows are poisoned: NaN, compared as bits)
+    assert torch.equal(got.view(torch.int16), again.view(torch.int16))
+    ref.check(got[:1400], *(x[:1400] for x in expect(case, late, q, 150, 4)))
+
+
+def test_output_that_is_only_16_byte_aligned():
+    case, starts, q = setup([(300, 900), (5, 5)], 8, 2, 64, 16, "f16", 100, 4, 6)
+    want, _ = run(case, starts, q, 100, 4)
+    dev = [from_bits(x, "f16").cuda() for x in (q, case["k"], case["v"])]
+    buf = torch.full((want.numel() + 8,), 7.0, dtype=torch.float16, device="cuda")
+    out = buf[8:].view(want.shape)
+    assert out.data_ptr() % 32 == 16
+    pk.pa_prefill_window(out, *dev, torch.from_numpy(case["tables"]).cuda(),
+                         torch.from_numpy(case["ctx"]).cuda(), torch.from_numpy(starts).cuda(),
+                         100, 4, case["scale"], pk.new_prefill_workspace())
+    assert torch.equal(out, want) and bool((buf[:8] == 7).all())
+
+
 def test_bad_inputs_are_reported():
     case, starts, q = setup([(40, 200), (50, 300)], 4, 2, 64, 16, "f16", 60, 4, 2, drop=False)
     good, st = run(case, starts, q, 60, 4)

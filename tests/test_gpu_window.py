@@ -209,3 +209,38 @@ def test_captured_and_on_another_stream():
     graphs[0].replay()
     case["ctx"] = np.array([64, 900, 17, 0], np.int32)
     assert torch.equal(got, run16(case, q, 100, 4)[0])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("Hq,q_len", [(4, 1), (16, 2)])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 2.5])
+def test_scales(dtype, Hq, q_len, scale):
+    case = make_case(len(CTX), Hq, 1, 128, 16, CTX, dtype=dtype, seed=12, poison=False)
+    mask = poison(case, q_len, 60, 4, drop=True)
+    for p in ("k", "v"):
+        case[p].transpose(0, 2, 1, 3)[mask] = NAN_BITS[dtype]
+    case["scale"] = scale
+    q = bits(inputs.randn((case["B"], q_len, Hq, 128), dtype, 3, stream=11))
+    out, st = run16(case, q, 60, 4)
+    assert st == 0
+    dbl = {x: from_bits(case[x], dtype).double() for x in ("k", "v")}
+    ref.check(out, *expected(case, from_bits(q, dtype).double(), dbl["k"], dbl["v"], 60, 4,
+                             u_p16(dtype, Hq * q_len)))
+
+
+def test_refusals():
+    case = make_case(2, 8, 2, 64, 16, [100, 20], dtype="f16", seed=2)
+    q = from_bits(case["q"], "f16").cuda()
+    ok = [torch.empty_like(q), q, from_bits(case["k"], "f16").cuda(), from_bits(case["v"], "f16").cuda(),
+          torch.from_numpy(case["tables"]).cuda(), torch.from_numpy(case["ctx"]).cuda(), 30, 4, 0.1,
+          pk.new_workspace(2, 8, 2, 64)]
+    pk.pa_decode_window(*ok)
+    for at, bad in ((1, q[:1]), (0, ok[0].bfloat16()), (2, ok[2].transpose(1, 2)), (4, ok[4].long()),
+                    (5, ok[5][:1]), (6, 0), (6, 3.5), (7, -1), (8, float("inf")),
+                    (9, ok[9][:64]), (3, ok[3].cpu())):
+        args = list(ok)
+        args[at] = bad
+        with pytest.raises(pk.PagedKVError):
+            pk.pa_decode_window(*args)
+    with pytest.raises(pk.PagedKVError):                       # 16-bit pools are not 8-bit ones
+        pk.pa_decode_window_e4m3_bs(*ok[:4], ok[2], ok[2], *ok[4:])
