@@ -111,7 +111,9 @@ size_t pa_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads
  *   block_tables   int32 [num_seqs][max_blocks_per_seq]
  *   context_lens   int32 [num_seqs]
  *   workspace      >= pa_decode_workspace_bytes(...) bytes, 256-byte aligned; its
- *                  contents on entry do not matter and are clobbered.
+ *                  contents on entry do not matter and are clobbered.  (A captured call that
+ *                  reported PA_DEV_TIMEOUT leaves its split unfinished there: zero the
+ *                  workspace before that graph is replayed.)
  *   dev_status     int32, nullable (see "Errors").
  *
  * The result is a deterministic function of the logical inputs: it does not depend

@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -149,13 +150,22 @@ bool encode_queries(CUtensorMap* map, const void* base, pa_dtype dtype, int head
   return r == CUDA_SUCCESS;
 }
 
-// Every call gets its own epoch so arrival counters left by earlier calls (or by an
-// aborted one) read as zero; 0 is skipped so a zeroed workspace also reads as zero.
-uint32_t next_epoch() {
-  static std::atomic<uint32_t> epoch{0};
-  uint32_t e = ++epoch;
-  if (e == 0) e = ++epoch;
-  return e;
+// Every call gets a tag of its own for its arrival counters (arrive_last), so that what earlier
+// calls, an aborted one or other programs left in the workspace reads as zero.  A count from a
+// start that differs from process to process, through a permutation of the 48-bit numbers (each
+// step, an odd factor or an exclusive-or with the upper half, can be undone): distinct for 2^48
+// calls, and like none of the numbers that memory is full of (small integers, pairs of them,
+// lengths, floats of a partial result), so a left-over word matches with chance 2^-48.
+unsigned long long next_tag() {
+  constexpr unsigned long long k48 = (1ull << 48) - 1;
+  static std::atomic<unsigned long long> count{
+      (unsigned long long)std::chrono::system_clock::now().time_since_epoch().count() ^
+      ((unsigned long long)reinterpret_cast<uintptr_t>(&count) << 13)};
+  unsigned long long x = ++count & k48;
+  x = ((x ^ (x >> 24)) * 0x9e3779b97f4bull) & k48;
+  x = ((x ^ (x >> 24)) * 0xc2b2ae3d27d5ull) & k48;
+  x ^= x >> 24;
+  return x << 16;
 }
 
 // Kernel mode -> its translation unit's dispatcher.
@@ -330,7 +340,7 @@ pa_status decode_impl(void* out, const void* q, const void* k_cache, const void*
   // weights (all 1)
   if (wide && a.scale_log2 == 0.f) a.scale_log2 = 1e-37f;
   a.v_scale = cx.v_scale;
-  a.epoch = next_epoch();
+  a.tag = next_tag();
   a.seq_start = cx.seq_start;
   a.chunk_members = cx.chunk_members;
   a.q_rows = cx.q_rows;

@@ -13,7 +13,7 @@
 //    caches or block_size <= 8), so a batch with a heavy-tailed
 //    length mix still gives every SM the same number of KV bytes.  A segment that
 //    straddles CTA ranges leaves one (max, sum, acc) partial per CTA in the
-//    workspace; the last of those CTAs to finish (an epoch-tagged arrival counter,
+//    workspace; the last of those CTAs to finish (a tagged arrival counter,
 //    released and acquired at GPU scope) merges them with a log-sum-exp reduction in
 //    CTA order, so the result does not depend on which CTA came last and no second
 //    kernel is needed.  The merge folds the partials in with a running maximum, several
@@ -131,13 +131,13 @@ struct DecodeArgs {
   const int32_t* context_lens;
   float* part_acc;              // [gridDim*2][kMaxGroup][D]
   float* part_ml;               // [gridDim*2][kMaxGroup][2]  (max, sum) in base 2
-  unsigned long long* counters; // [gridDim] arrival counters: (epoch << 32) | arrivals
+  unsigned long long* counters; // [gridDim] arrival counters: tag | arrivals (arrive_last)
   int32_t* status;              // nullable
   int num_seqs, num_q_heads, num_kv_heads, group, max_blocks, num_blocks, ctx_cap;
   int q_len;                    // new tokens per sequence (query rows [seq][q_len][Hq][D])
   int ncol;                     // query rows per kv head: group * q_len (MMA columns)
   float scale_log2;             // scale * log2(e)
-  uint32_t epoch;               // distinct per call: counters of older calls read as zero
+  unsigned long long tag;       // distinct per call, low 16 bits zero
   // cascade (kPrefix / kSuffix launches only)
   const int32_t* seq_start;     // kSuffix: first token of each sequence's own part
   const int32_t* chunk_members; // kPrefix: [num_seqs][q_len] member sequences, -1 pad
@@ -272,28 +272,32 @@ __device__ __forceinline__ unsigned long long add_acq_rel_gpu(unsigned long long
   return old;
 }
 
-// Arrival on a split segment's counter ((epoch << 32) | arrivals); another call's tag reads as
-// zero.  True for the last of n contributors, which resets the counter.  One round trip in the
+// Arrival on a split segment's counter: a call's 48-bit tag above 16 bits of arrivals (a segment
+// has at most one contributor a CTA); a word without this call's tag reads as zero.  The
+// counters are never cleared for a call and a workspace may hold anything on entry, so tags are
+// spread over the 48 bits (next_tag): numbers that counted up from 1 were found in memory that
+// had held indices or lengths, and read as arrivals already made.  True for the last of n
+// contributors, which resets the counter.  One round trip in the
 // usual case: the first CTA of a segment (whose portion is the end of its range) is usually
 // the last to arrive, the others the first.  After a wrong guess the value that came back
 // carries this call's tag as a rule, and an addition arrives without competing.  (Compare-and-
 // swap alone let one contributor through a round trip: with 37 to a segment, as one sequence
 // over 296 CTAs has, 68 us against 42.)
-__device__ __forceinline__ bool arrive_last(unsigned long long* ctr, uint32_t epoch, int n,
+constexpr unsigned long long kArrivalBits = 0xffffull;
+__device__ __forceinline__ bool arrive_last(unsigned long long* ctr, unsigned long long tag, int n,
                                             bool first) {
-  const unsigned long long tag = (unsigned long long)epoch << 32;
   unsigned long long old = first ? tag | (uint32_t)(n - 1) : 0ull, now;
   for (;;) {
-    now = (uint32_t)(old >> 32) == epoch ? old + 1 : tag | 1ull;
+    now = (old & ~kArrivalBits) == tag ? old + 1 : tag | 1ull;
     const unsigned long long prev = cas_acq_rel_gpu(ctr, old, now);
     if (prev == old) break;
-    if ((uint32_t)(prev >> 32) == epoch) {
+    if ((prev & ~kArrivalBits) == tag) {
       now = add_acq_rel_gpu(ctr, 1ull) + 1;
       break;
     }
     old = prev;
   }
-  const bool last = (int)(uint32_t)now == n;
+  const bool last = (int)(now & kArrivalBits) == n;
   if (last) st_relaxed_gpu(ctr, 0ull);             // every contributor has arrived
   return last;
 }
@@ -1634,7 +1638,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(KV8, NT, BS))
         named_bar_sync(1, kConsumerThreads);
         const SplitDesc dsc = desc[mt.qslot];
         if (tid == 0) {
-          *last_flag = arrive_last(a.counters + dsc.cf, a.epoch, dsc.ncontrib, dsc.cf == c);
+          *last_flag = arrive_last(a.counters + dsc.cf, a.tag, dsc.ncontrib, dsc.cf == c);
         }
         named_bar_sync(1, kConsumerThreads);
         if (*last_flag) merge_split<T, D, NT, MODE>(a, dsc, *total_s, G, group, tid);

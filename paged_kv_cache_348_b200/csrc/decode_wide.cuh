@@ -1029,7 +1029,7 @@ __global__ void __launch_bounds__(wide_threads(NC), 1)
           named_bar_sync(1, kWideSoftThreads);
           const SplitDesc dsc = desc[mt.qslot];
           if (tid == 0) {
-            *last_flag = arrive_last(a.counters + dsc.cf, a.epoch, dsc.ncontrib, dsc.cf == c);
+            *last_flag = arrive_last(a.counters + dsc.cf, a.tag, dsc.ncontrib, dsc.cf == c);
           }
           named_bar_sync(1, kWideSoftThreads);
           if (*last_flag) merge_wide<T, D, MODE, kWideSoftThreads>(a, dsc, *total_s, G, tid);
