@@ -477,7 +477,9 @@ pa_status pa_copy_blocks(void* const* k_caches, void* const* v_caches, int num_l
  * (pa_cache_append_e4m3_bs): k_scales, v_scales are HOST arrays of num_layers device pointers
  * to float [num_blocks][num_kv_heads].  A new block's scale is the one that the row at its
  * offset 0 fixes (the append's rule, from that row's values scale * code), and each value of
- * its rows becomes the E4M3 code of value / scale (nearest even, clamped to 448).
+ * its rows becomes the E4M3 code of value / scale (nearest even, clamped to 448).  Where that
+ * row is skipped the first row of the block that is not fixes the scale; a block without one
+ * keeps its scale.
  */
 pa_status pa_compact_tokens(void* const* k_caches, void* const* v_caches, int num_layers,
                             const int32_t* src_tables, int src_blocks_per_seq,

@@ -134,9 +134,9 @@ __global__ void __launch_bounds__(kCompactThreads, 4)
 }
 
 // 8-bit (E4M3) pools with per-(block, kv head) scales: a kept row's values are scale * code of
-// its old block; a new block's scale is the one that its first row fixes (e4m3_block_scale of
-// that row's largest magnitude, the rule of the append), and every row of the block is
-// quantised with it.  The powers of two make value / scale exact, so a code changes only
+// its old block; a new block's scale is the one that its first moved row fixes (e4m3_block_scale
+// of that row's largest magnitude, the rule of the append; the row at offset 0 unless that one
+// has to be left out), and every row of the block is quantised with it.  The powers of two make value / scale exact, so a code changes only
 // where the scale grew past its low bits or shrank below its magnitude.
 //
 // Half the bytes of a 16-bit row and a conversion both ways: what bounds it is the latency of
@@ -144,8 +144,9 @@ __global__ void __launch_bounds__(kCompactThreads, 4)
 // 2: 48 registers, several CTAs an SM), the next chunk's rows are loaded before this one's are
 // stored (reading ahead is always safe: rows still to be stored over lie below every position
 // that is still to be read), block and offset come by shift and mask, and only the rows that
-// fix a scale search their maximum.  16 sequences x 8 heads x 2 layers of 700 rows: 30.4 us,
-// 2.9 TB/s (57.0 with kU = 4 and neither of these; the bytes alone take 13.6).
+// fix a scale search their maximum.  16 sequences x 8 heads x 2 layers of 700 rows: 31.3 us,
+// 2.8 TB/s (57.0 with kU = 4 and neither of these; the bytes alone take 13.6).  Taking the rows
+// that fix a scale from what is moved, not from the offset, is 0.9 us of it.
 template <int CPR>
 __global__ void __launch_bounds__(kCompactThreads, 4)
     pa_compact_e4m3_bs_kernel(const __grid_constant__ ScaledLayerPtrs P, const CompactArgs a,
@@ -154,8 +155,11 @@ __global__ void __launch_bounds__(kCompactThreads, 4)
   constexpr int kRows = kCompactThreads * kU / CPR;       // a multiple of every block size
   static_assert(kRows % 32 == 0 && kRows <= kCompactThreads, "whole blocks, one place a thread");
   // places of four chunks: chunk c + 2's are found while the slowest warp may still be storing
-  // chunk c - 1
-  __shared__ int src_s[4][kRows], dst_s[4][kRows];
+  // chunk c - 1.  src_s: twice the old row, plus one where the row fixes its block's scale (a pool
+  // has fewer than 2^31 rows)
+  __shared__ uint32_t src_s[4][kRows];
+  __shared__ int dst_s[4][kRows];
+  constexpr uint32_t kNone = 0xffffffffu;                 // src_s: nothing to move
   __shared__ float new_s[2][kRows];                       // a chunk's new block scales
   pdl_wait();
   pdl_trigger();
@@ -173,23 +177,30 @@ __global__ void __launch_bounds__(kCompactThreads, 4)
       const int i = c * kRows + tid;
       int src = -1, dst = -1;
       if (i < n && !compact_row(a, keep, s, h, ctx, i, src, dst)) src = dst = -1;
-      src_s[c & 3][tid] = src;
+      // the first row of each block that is moved at all: no moved row between its block's
+      // start and it (whole warps: kRows is a multiple of 32, and so is no block wider)
+      const int r = tid & 31;
+      const uint32_t moved = __ballot_sync(0xffffffffu, src >= 0);
+      const uint32_t before = ((1u << r) - 1u) & ~((1u << (r & ~in)) - 1u);
+      src_s[c & 3][tid] = src < 0 ? kNone : 2u * (uint32_t)src + !(moved & before);
       dst_s[c & 3][tid] = dst;
     }
   };
   struct Piece {
     uint4 x;
     float sc;
+    bool lead;
   };
   auto load = [&](int c, Piece (&p)[kU]) {
     if (c >= nc) return;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int e = u * kCompactThreads + tid;
-      const int src = src_s[c & 3][e / CPR];
+      const uint32_t src2 = src_s[c & 3][e / CPR], src = src2 >> 1;
       p[u].x = make_uint4(0u, 0u, 0u, 0u);
       p[u].sc = 1.f;
-      if (src >= 0) {
+      p[u].lead = src2 != kNone && (src2 & 1u);
+      if (src2 != kNone) {
         p[u].x = *(base + (long long)src * CPR + e % CPR);
         p[u].sc = scales[src >> lg];                      // = block * heads + head
       }
@@ -203,11 +214,11 @@ __global__ void __launch_bounds__(kCompactThreads, 4)
   for (int c = 0; c < nc; ++c) {
     load(c + 1, nxt);
     places(c + 2);
-    // the first row of each new block fixes its scale
+    // the first moved row of each new block fixes its scale
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int r = (u * kCompactThreads + tid) / CPR;
-      const bool first = (r & in) == 0;
+      const bool first = now[u].lead;
       if (!__any_sync(0xffffffffu, first)) continue;
       const uint32_t w[4] = {now[u].x.x, now[u].x.y, now[u].x.z, now[u].x.w};
       float am = 0.f;
@@ -243,7 +254,7 @@ __global__ void __launch_bounds__(kCompactThreads, 4)
                  (f32x2_to_e4m3x2(f1.x * sc * inv, f1.y * sc * inv) << 16);
         }
         *(base + (long long)dst * CPR + e % CPR) = make_uint4(q[0], q[1], q[2], q[3]);
-        if ((r & in) == 0 && e % CPR == 0) scales[dst >> lg] = ns;
+        if (now[u].lead && e % CPR == 0) scales[dst >> lg] = ns;
       }
       now[u] = nxt[u];
     }
