@@ -665,7 +665,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (it.tiles) entries(0, cur);
         for (int i = 0; ok && i < it.tiles; ++i) {
           if (i + 1 < it.tiles) entries(i + 1, nxt);
-          int y[kE];                                // row coordinate of the box (out of range: zeros)
+          // row coordinate of the box; out of range (zeros) for a page with a bad id
+          int y[kE];
           [[maybe_unused]] bool patch = false;      // its V rows are copied one by one
           bool load_k = false;
 #pragma unroll
@@ -673,9 +674,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const int t = pf_pos(it, i * kPfKeys + (x * 32 + lane) * H);
             y[x] = rows_total;
             if (x * 32 + lane < kBoxes && needed(t, H) && (BS != 1 || seen(t))) {
+              load_k = true;
               if ((unsigned)cur[x] < (unsigned)a.num_blocks) {
                 y[x] = (cur[x] * Hkv + it.kvh) * BS + t % BS;
-                load_k = true;
                 patch = BS != 1 && !sure(t, H);
               } else if (a.status) {
                 atomicOr(a.status, DEV_BAD_BLOCK_ID);
