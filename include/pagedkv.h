@@ -199,7 +199,9 @@ pa_status pa_decode_window_e4m3_bs(void* out, const void* q, const void* k_cache
  * a window of context_lens[s] or more is the plain causal mask.  A token with p < 0 sees
  * nothing: its row is zero.  What lies outside every window may hold anything, as for
  * pa_decode_window; the rows that some new token of a sequence sees must be finite for all
- * of its tokens.
+ * of its tokens.  A row with a visible score of +inf or NaN (an overflow, or a query that is not
+ * finite) is NaN and no other row is touched by it; scores of -inf have no weight, and a row
+ * that has only those is zero.
  *
  *   q, out         [total_q][num_q_heads][head_dim]; rows of no sequence are not written
  *   q_starts       device int32 [num_seqs + 1], ascending (equal: no new tokens), in

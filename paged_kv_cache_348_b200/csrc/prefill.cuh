@@ -383,12 +383,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t* x = s + 32 * c;
-            mx[c] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+            mx[c] = max2_nan(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
             for (int j = 2; j < 32; j += 2)
-              mx[c] = max3(mx[c], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+              mx[c] = max3_nan(mx[c], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
           }
-          const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          const float mt = max2_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]);
+          // a visible score of +inf or NaN makes the row NaN, as the formula's inf - inf does
+          // (the weights alone would lose it where they come from the polynomial)
+          if (!(mt < INFINITY)) l = NAN;
           // the reference moves on a row's first visible tile and past a gap of 2^8
           const bool move = mt > m && (m == -INFINITY || (mt - m) * sc > kRescaleLog2);
           // the P V of the tile before has read P and is done with O
@@ -465,6 +468,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (!ok) break;
         vph ^= 1u;
         tc_fence_after();
+        // a row whose scores were all -inf never had a reference: what the polynomial made of
+        // them (2^-126) is no weight
+        if (m == -INFINITY && l == l) l = 0.f;
       }
       // output rows; a row that sees nothing is zero.  A thread holds a row of O, so 64
       // columns at a time go through the warp's staging area and out as 128 contiguous bytes of

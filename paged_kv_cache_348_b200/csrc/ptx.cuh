@@ -215,10 +215,15 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 
-// Maximum of three.
-__device__ __forceinline__ float max3(float a, float b, float c) {
+// Maximum of two and of three; NaN where an operand is.
+__device__ __forceinline__ float max2_nan(float a, float b) {
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 // Two binary32 values in one 64-bit register, and arithmetic on both at once.
@@ -246,7 +251,7 @@ __device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
 // x = n + f with n the nearest whole number (added to 1.5 * 2^23 it sits in the low bits), 2^f
 // on [-1/2, 1/2] by the degree-4 polynomial of least maximum relative error (2.6e-6; fitted
 // with the exchange algorithm of Remez), n added to the exponent.  For x in [-126, 127);
-// smaller values are taken as -126.
+// smaller values, and NaN, are taken as -126: the caller sees to rows where that matters.
 __device__ __forceinline__ float2 ex2_poly_f2(uint64_t x) {
   const float2 c = unpack_f2(x);
   x = pack_f2(fmaxf(c.x, -126.f), fmaxf(c.y, -126.f));
