@@ -20,7 +20,6 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
-#include <deque>
 #include <new>
 #include <unordered_map>
 #include <unordered_set>
@@ -38,14 +37,22 @@ struct pa_block_manager {
   };
   int32_t num_blocks = 0, block_size = 0;
   std::vector<int32_t> ref;      // reference count per physical block
-  std::deque<int32_t> free;      // free blocks, handed out from the front
+  // free blocks, handed out from the front: a ring with room for all of them, so that neither
+  // taking nor giving back a block allocates
+  std::vector<int32_t> ring;
+  int32_t head = 0, num_free = 0;
   std::unordered_map<int32_t, Seq> seqs;
   int32_t next_id = 0;
 
+  void push_free(int32_t b) {
+    const int64_t at = (int64_t)head + num_free++;
+    ring[(size_t)(at < num_blocks ? at : at - num_blocks)] = b;
+  }
   int32_t take() {               // caller has checked that a block is free
-    const int32_t b = free.front();
-    free.pop_front();
-    ref[b] = 1;
+    const int32_t b = ring[(size_t)head];
+    head = head + 1 < num_blocks ? head + 1 : 0;
+    --num_free;
+    ref[(size_t)b] = 1;
     return b;
   }
   Seq* find(int32_t id) {
@@ -62,10 +69,25 @@ struct pa_block_manager {
     return s && !s->swapped ? s : nullptr;
   }
   void drop(int32_t b) {         // one reference less; a block nobody holds is free again
-    if (--ref[(size_t)b] == 0) free.push_back(b);
+    if (--ref[(size_t)b] == 0) push_free(b);
   }
   int64_t blocks_for(int64_t tokens) const { return (tokens + block_size - 1) / block_size; }
 };
+
+namespace {
+
+// No exception leaves a C entry.  The calls allocate all they need before their first change, so
+// that one which runs out of memory has changed nothing.
+template <typename Fn>
+pa_status guarded(Fn fn) {
+  try {
+    return fn();
+  } catch (...) {
+    return PA_ERR_NO_MEMORY;
+  }
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -76,22 +98,27 @@ pa_status pa_bm_create(int num_blocks, int block_size, const int32_t* free_order
   if (num_blocks <= 0 || block_size <= 0) return PA_ERR_INVALID;
   pa_block_manager* bm = new (std::nothrow) pa_block_manager();
   if (!bm) return PA_ERR_NO_MEMORY;
-  bm->num_blocks = num_blocks;
-  bm->block_size = block_size;
-  bm->ref.assign((size_t)num_blocks, 0);
-  if (free_order) {
+  const pa_status r = guarded([&] {
+    bm->num_blocks = num_blocks;
+    bm->block_size = block_size;
+    bm->ref.assign((size_t)num_blocks, 0);
+    bm->ring.resize((size_t)num_blocks);
+    if (!free_order) {
+      for (int i = 0; i < num_blocks; ++i) bm->push_free(i);
+      return PA_OK;
+    }
     std::vector<uint8_t> seen((size_t)num_blocks, 0);
     for (int i = 0; i < num_blocks; ++i) {
       const int32_t b = free_order[i];
-      if (b < 0 || b >= num_blocks || seen[(size_t)b]) {
-        delete bm;
-        return PA_ERR_INVALID;   // not a permutation of the pool
-      }
+      if (b < 0 || b >= num_blocks || seen[(size_t)b]) return PA_ERR_INVALID;   // no permutation
       seen[(size_t)b] = 1;
-      bm->free.push_back(b);
+      bm->push_free(b);
     }
-  } else {
-    for (int i = 0; i < num_blocks; ++i) bm->free.push_back(i);
+    return PA_OK;
+  });
+  if (r != PA_OK) {
+    delete bm;
+    return r;
   }
   *out = bm;
   return PA_OK;
@@ -99,7 +126,7 @@ pa_status pa_bm_create(int num_blocks, int block_size, const int32_t* free_order
 
 void pa_bm_destroy(pa_block_manager* bm) { delete bm; }
 
-int pa_bm_free_blocks(const pa_block_manager* bm) { return bm ? (int)bm->free.size() : -1; }
+int pa_bm_free_blocks(const pa_block_manager* bm) { return bm ? bm->num_free : -1; }
 
 int pa_bm_refcount(const pa_block_manager* bm, int block) {
   if (!bm || block < 0 || block >= bm->num_blocks) return -1;
@@ -109,28 +136,30 @@ int pa_bm_refcount(const pa_block_manager* bm, int block) {
 pa_status pa_bm_allocate(pa_block_manager* bm, int num_tokens, int32_t* seq_id) {
   if (!bm || !seq_id || num_tokens < 0) return PA_ERR_INVALID;
   const int64_t need = bm->blocks_for(num_tokens);
-  if (need > (int64_t)bm->free.size()) return PA_ERR_NO_BLOCKS;
-  pa_block_manager::Seq s;
-  s.table.reserve((size_t)need);
-  for (int64_t i = 0; i < need; ++i) s.table.push_back(bm->take());
-  s.len = num_tokens;
-  const int32_t id = bm->next_id++;
-  bm->seqs.emplace(id, std::move(s));
-  *seq_id = id;
-  return PA_OK;
+  if (need > bm->num_free) return PA_ERR_NO_BLOCKS;
+  return guarded([&] {
+    pa_block_manager::Seq fresh;
+    fresh.table.reserve((size_t)need);
+    pa_block_manager::Seq& s = bm->seqs.emplace(bm->next_id, std::move(fresh)).first->second;
+    for (int64_t i = 0; i < need; ++i) s.table.push_back(bm->take());
+    s.len = num_tokens;
+    *seq_id = bm->next_id++;
+    return PA_OK;
+  });
 }
 
 pa_status pa_bm_fork(pa_block_manager* bm, int32_t seq, int32_t* child) {
   if (!bm || !child) return PA_ERR_INVALID;
   const pa_block_manager::Seq* p = bm->resident(seq);
   if (!p) return PA_ERR_INVALID;
-  pa_block_manager::Seq c = *p;                  // shares every block of the parent
-  for (int32_t b : c.table)
-    if (b >= 0) ++bm->ref[(size_t)b];
-  const int32_t id = bm->next_id++;
-  bm->seqs.emplace(id, std::move(c));
-  *child = id;
-  return PA_OK;
+  return guarded([&] {
+    // shares every block of the parent (whose place in the map does not move)
+    const pa_block_manager::Seq& c = bm->seqs.emplace(bm->next_id, *p).first->second;
+    for (int32_t b : c.table)
+      if (b >= 0) ++bm->ref[(size_t)b];
+    *child = bm->next_id++;
+    return PA_OK;
+  });
 }
 
 pa_status pa_bm_append_tokens(pa_block_manager* bm, const int32_t* seqs, int n, int64_t* slots,
@@ -138,63 +167,69 @@ pa_status pa_bm_append_tokens(pa_block_manager* bm, const int32_t* seqs, int n, 
   if (!bm || n < 0 || (n && (!seqs || !slots || !cow_pairs || !num_cow))) return PA_ERR_INVALID;
   if (num_cow) *num_cow = 0;
   if (n == 0) return PA_OK;
-  // Dry run on copies of the touched state: how many fresh blocks the whole batch needs
-  // (a new logical block, or a private copy of a shared partial block), so that a batch
-  // the pool cannot serve changes nothing.
-  struct Sim {
-    int64_t len, nblk;
-    std::vector<int64_t> priv;   // logical blocks made private earlier in this batch
-  };
-  std::unordered_map<int32_t, Sim> sim;
-  std::unordered_map<int32_t, int32_t> ref;
-  int64_t need = 0;
-  for (int i = 0; i < n; ++i) {
-    const pa_block_manager::Seq* s = bm->resident(seqs[i]);
-    if (!s) return PA_ERR_INVALID;
-    Sim& m = sim.try_emplace(seqs[i], Sim{s->len, (int64_t)s->table.size(), {}}).first->second;
-    const int64_t lb = m.len / bm->block_size;
-    if (lb == m.nblk) {
-      ++need;
-      ++m.nblk;
-      m.priv.push_back(lb);
-    } else {
-      bool priv = false;
-      for (int64_t x : m.priv) priv |= x == lb;
-      if (!priv) {
-        const int32_t b = s->table[(size_t)lb];
-        auto ri = ref.find(b);
-        const int32_t r = ri == ref.end() ? bm->ref[(size_t)b] : ri->second;
-        if (r > 1) {
-          ++need;
-          ref[b] = r - 1;
-          m.priv.push_back(lb);
+  return guarded([&] {
+    // Dry run on copies of the touched state: how many fresh blocks the whole batch needs
+    // (a new logical block, or a private copy of a shared partial block), so that a batch
+    // the pool cannot serve changes nothing.
+    struct Sim {
+      int64_t len, nblk;
+      std::vector<int64_t> priv;   // logical blocks made private earlier in this batch
+    };
+    std::unordered_map<int32_t, Sim> sim;
+    std::unordered_map<int32_t, int32_t> ref;
+    int64_t need = 0;
+    for (int i = 0; i < n; ++i) {
+      const pa_block_manager::Seq* s = bm->resident(seqs[i]);
+      if (!s) return PA_ERR_INVALID;
+      Sim& m = sim.try_emplace(seqs[i], Sim{s->len, (int64_t)s->table.size(), {}}).first->second;
+      const int64_t lb = m.len / bm->block_size;
+      if (lb == m.nblk) {
+        ++need;
+        ++m.nblk;
+        m.priv.push_back(lb);
+      } else {
+        bool priv = false;
+        for (int64_t x : m.priv) priv |= x == lb;
+        if (!priv) {
+          const int32_t b = s->table[(size_t)lb];
+          auto ri = ref.find(b);
+          const int32_t r = ri == ref.end() ? bm->ref[(size_t)b] : ri->second;
+          if (r > 1) {
+            ++need;
+            ref[b] = r - 1;
+            m.priv.push_back(lb);
+          }
         }
       }
+      ++m.len;
     }
-    ++m.len;
-  }
-  if (need > (int64_t)bm->free.size()) return PA_ERR_NO_BLOCKS;
-  int nc = 0;
-  for (int i = 0; i < n; ++i) {
-    pa_block_manager::Seq& s = *bm->find(seqs[i]);
-    const int64_t pos = s.len;
-    const int64_t lb = pos / bm->block_size, off = pos % bm->block_size;
-    if (lb == (int64_t)s.table.size()) {
-      s.table.push_back(bm->take());
-    } else if (bm->ref[(size_t)s.table[(size_t)lb]] > 1) {
-      const int32_t src = s.table[(size_t)lb];
-      const int32_t dst = bm->take();
-      --bm->ref[(size_t)src];
-      s.table[(size_t)lb] = dst;
-      cow_pairs[2 * nc] = src;
-      cow_pairs[2 * nc + 1] = dst;
-      ++nc;
+    if (need > bm->num_free) return PA_ERR_NO_BLOCKS;
+    for (auto& [id, m] : sim) {              // room for the new entries, doubled as they grow
+      std::vector<int32_t>& t = bm->find(id)->table;
+      if (t.capacity() < (size_t)m.nblk) t.reserve(std::max((size_t)m.nblk, 2 * t.capacity()));
     }
-    s.len = pos + 1;
-    slots[i] = (int64_t)s.table[(size_t)lb] * bm->block_size + off;
-  }
-  *num_cow = nc;
-  return PA_OK;
+    int nc = 0;
+    for (int i = 0; i < n; ++i) {
+      pa_block_manager::Seq& s = *bm->find(seqs[i]);
+      const int64_t pos = s.len;
+      const int64_t lb = pos / bm->block_size, off = pos % bm->block_size;
+      if (lb == (int64_t)s.table.size()) {
+        s.table.push_back(bm->take());
+      } else if (bm->ref[(size_t)s.table[(size_t)lb]] > 1) {
+        const int32_t src = s.table[(size_t)lb];
+        const int32_t dst = bm->take();
+        --bm->ref[(size_t)src];
+        s.table[(size_t)lb] = dst;
+        cow_pairs[2 * nc] = src;
+        cow_pairs[2 * nc + 1] = dst;
+        ++nc;
+      }
+      s.len = pos + 1;
+      slots[i] = (int64_t)s.table[(size_t)lb] * bm->block_size + off;
+    }
+    *num_cow = nc;
+    return PA_OK;
+  });
 }
 
 pa_status pa_bm_release(pa_block_manager* bm, int32_t seq) {
@@ -265,11 +300,11 @@ pa_status pa_bm_swap_out(pa_block_manager* bm, int32_t seq, int32_t* blocks, int
   pa_block_manager::Seq* s = bm->find(seq);
   if (!s || s->swapped || (!s->table.empty() && !blocks)) return PA_ERR_INVALID;
   if (s->holes) {
-    try {
+    const pa_status r = guarded([&] {
       s->hole.assign(s->table.size(), 0);
-    } catch (...) {
-      return PA_ERR_NO_MEMORY;
-    }
+      return PA_OK;
+    });
+    if (r != PA_OK) return r;
   }
   size_t n = 0;
   for (size_t i = 0; i < s->table.size(); ++i) {
@@ -290,8 +325,12 @@ pa_status pa_bm_swap_in(pa_block_manager* bm, int32_t seq, int32_t* blocks, int*
   if (!s || !s->swapped) return PA_ERR_INVALID;
   const int64_t all = bm->blocks_for(s->len), need = all - s->holes;
   if (need && !blocks) return PA_ERR_INVALID;
-  if (need > (int64_t)bm->free.size()) return PA_ERR_NO_BLOCKS;
-  s->table.resize((size_t)all);
+  if (need > bm->num_free) return PA_ERR_NO_BLOCKS;
+  const pa_status r = guarded([&] {
+    s->table.resize((size_t)all);
+    return PA_OK;
+  });
+  if (r != PA_OK) return r;
   int64_t k = 0;
   for (int64_t i = 0; i < all; ++i)
     s->table[(size_t)i] = s->holes && s->hole[(size_t)i] ? -1 : (blocks[k++] = bm->take());
@@ -326,7 +365,7 @@ pa_status pa_bm_drop_window(pa_block_manager* bm, int32_t seq, int window, int n
 pa_status pa_bm_compact(pa_block_manager* bm, const int32_t* seqs, const int32_t* new_lens, int n,
                         int width, int32_t fill, int32_t* tables) {
   if (!bm || n < 0 || (n && (!seqs || !new_lens || !tables || width <= 0))) return PA_ERR_INVALID;
-  try {
+  return guarded([&] {
     // every sequence once, and what the batch needs: a new table keeps the entries that its
     // sequence alone holds (counts as they are before the call, so that a block that two
     // sequences of the batch share is a source for both and a destination for neither)
@@ -348,7 +387,7 @@ pa_status pa_bm_compact(pa_block_manager* bm, const int32_t* seqs, const int32_t
         need += !own;
       }
     }
-    if (need > (int64_t)bm->free.size()) return PA_ERR_NO_BLOCKS;
+    if (need > bm->num_free) return PA_ERR_NO_BLOCKS;
     // fresh blocks first, from the front of the queue; what is left over goes to its back
     for (int i = 0; i < n; ++i)
       for (int32_t& b : fresh[(size_t)i])
@@ -364,11 +403,8 @@ pa_status pa_bm_compact(pa_block_manager* bm, const int32_t* seqs, const int32_t
       s.len = new_lens[i];
       s.holes = 0;
     }
-  } catch (...) {
-    return PA_ERR_NO_MEMORY;     // (only before the first change: nothing after it allocates
-                                 // but the free queue's tail)
-  }
-  return PA_OK;
+    return PA_OK;
+  });
 }
 
 }  // extern "C"
@@ -473,27 +509,31 @@ pa_status pa_plan_cascade(const int32_t* block_tables, int max_blocks_per_seq,
     for (int64_t j = 0; j < (c + block_size - 1) / block_size; ++j)
       if (row[j] < 0) return PA_ERR_INVALID;       // a page that was given back
   }
-  return plan_rows(
-      num_seqs, block_size, group, chunk_width,
-      [&](int i) { return block_tables + (int64_t)i * max_blocks_per_seq; },
-      [&](int i) { return (int64_t)context_lens[i]; }, prefix_lens, chunk_members,
-      chunk_prefix_lens, num_chunks, chunk_width_out);
+  return guarded([&] {
+    return plan_rows(
+        num_seqs, block_size, group, chunk_width,
+        [&](int i) { return block_tables + (int64_t)i * max_blocks_per_seq; },
+        [&](int i) { return (int64_t)context_lens[i]; }, prefix_lens, chunk_members,
+        chunk_prefix_lens, num_chunks, chunk_width_out);
+  });
 }
 
 pa_status pa_bm_plan_cascade(const pa_block_manager* bm, const int32_t* seqs, int n, int group,
                              int chunk_width, int32_t* prefix_lens, int32_t* chunk_members,
                              int32_t* chunk_prefix_lens, int* num_chunks, int* chunk_width_out) {
   if (!bm || n < 0 || (n && !seqs)) return PA_ERR_INVALID;
-  std::vector<const pa_block_manager::Seq*> rows((size_t)n);
-  for (int i = 0; i < n; ++i) {
-    rows[(size_t)i] = bm->resident(seqs[i]);
-    if (!rows[(size_t)i] || rows[(size_t)i]->holes) return PA_ERR_INVALID;
-  }
-  return plan_rows(
-      n, bm->block_size, group, chunk_width,
-      [&](int i) { return rows[(size_t)i]->table.data(); },
-      [&](int i) { return rows[(size_t)i]->len; }, prefix_lens, chunk_members, chunk_prefix_lens,
-      num_chunks, chunk_width_out);
+  return guarded([&] {
+    std::vector<const pa_block_manager::Seq*> rows((size_t)n);
+    for (int i = 0; i < n; ++i) {
+      rows[(size_t)i] = bm->resident(seqs[i]);
+      if (!rows[(size_t)i] || rows[(size_t)i]->holes) return PA_ERR_INVALID;
+    }
+    return plan_rows(
+        n, bm->block_size, group, chunk_width,
+        [&](int i) { return rows[(size_t)i]->table.data(); },
+        [&](int i) { return rows[(size_t)i]->len; }, prefix_lens, chunk_members,
+        chunk_prefix_lens, num_chunks, chunk_width_out);
+  });
 }
 
 }  // extern "C"
