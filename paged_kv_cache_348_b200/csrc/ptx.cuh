@@ -324,9 +324,6 @@ __device__ __forceinline__ bool elect_one() {
   return x != 0;
 }
 // 32 consecutive 32-bit columns of this warp's 32 lanes (registers r[0..31]).
-#define PKV_R8(r, i) \
-  "r"((r)[i]), "r"((r)[i + 1]), "r"((r)[i + 2]), "r"((r)[i + 3]), "r"((r)[i + 4]), \
-      "r"((r)[i + 5]), "r"((r)[i + 6]), "r"((r)[i + 7])
 #define PKV_W8(r, i) \
   "=r"((r)[i]), "=r"((r)[i + 1]), "=r"((r)[i + 2]), "=r"((r)[i + 3]), "=r"((r)[i + 4]), \
       "=r"((r)[i + 5]), "=r"((r)[i + 6]), "=r"((r)[i + 7])
@@ -337,14 +334,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : PKV_W8(r, 0), PKV_W8(r, 8), PKV_W8(r, 16), PKV_W8(r, 24)
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      PKV_R8(r, 0), PKV_R8(r, 8), PKV_R8(r, 16), PKV_R8(r, 24)
-      : "memory");
-}
-#undef PKV_R8
 #undef PKV_W8
 // 16 consecutive 32-bit columns of this warp's 32 lanes: thread i gets lane (base lane + i).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
