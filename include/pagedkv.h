@@ -60,7 +60,7 @@ typedef enum {
   PA_ERR_UNSUPPORTED = 2,  /* head_dim, block_size, dtype or group size not built */
   PA_ERR_CUDA = 3,         /* a CUDA runtime/driver call or launch failed */
   PA_ERR_NO_BLOCKS = 4,    /* block manager: not enough free blocks; nothing was changed */
-  PA_ERR_NO_MEMORY = 5     /* block manager: host memory allocation failed */
+  PA_ERR_NO_MEMORY = 5     /* block manager: host memory ran out; nothing was changed */
 } pa_status;
 
 typedef enum { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
@@ -104,6 +104,8 @@ size_t pa_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads
  * context_lens[s] counts every cached token, the newest one included (append runs
  * first).  A length of 0 gives an all-zero output row.  Block-table entries past
  * ceil(context_lens[s]/block_size) and cache slots past the last token are never read.
+ * Queries are expected finite and scores scale * <q, K> below 2^23 in magnitude: else the query
+ * row concerned, and no other, is undefined.
  *
  *   out            [num_seqs][num_q_heads][head_dim]            (written)
  *   q              [num_seqs][num_q_heads][head_dim]
