@@ -491,11 +491,17 @@ def pa_decode_append_e4m3_bs(out, q, k_cache8, v_cache8, k_scales, v_scales, k_n
     return out
 
 
-def _here(what, *tensors):
-    """The calls run on the current device: tensors of another one are refused."""
+def _here(what, status, *tensors):
+    """The calls run on the current device: tensors of another one are refused, and a status that
+    the kernels' 32-bit writes would not fit."""
     dev = torch.cuda.current_device()
+    if status is not None:
+        _need(status, "status", dtype=torch.int32)
+        if status.numel() < 1:
+            raise PagedKVError("%s: status holds no element" % what)
+        tensors += (status,)
     for t in tensors:
-        if t is not None and t.get_device() != dev:
+        if t.get_device() != dev:
             raise PagedKVError("%s: tensors on %s, the current device is cuda:%d"
                                % (what, t.device, dev))
 
@@ -535,8 +541,8 @@ def pa_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, windo
     _need(v_cache, "v_cache", dtype=q.dtype, ndim=4)
     B, QL, Hq, D, N, Hkv, bs = _window_shapes("pa_decode_window", out, q, k_cache, v_cache,
                                               block_tables, context_lens, workspace)
-    _here("pa_decode_window", out, q, k_cache, v_cache, block_tables, context_lens, workspace,
-          status)
+    _here("pa_decode_window", status, out, q, k_cache, v_cache, block_tables, context_lens,
+          workspace)
     rc = load().pa_decode_window(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
         B, QL, Hq, Hkv, D, bs, block_tables.shape[1], N, _whole(window, "window"),
@@ -559,8 +565,8 @@ def pa_decode_window_e4m3_bs(out, q, k_cache8, v_cache8, k_scales, v_scales, blo
                                               v_cache8, block_tables, context_lens, workspace)
     if k_scales.shape != (N, Hkv) or v_scales.shape != (N, Hkv):
         raise PagedKVError("pa_decode_window_e4m3_bs: inconsistent shapes")
-    _here("pa_decode_window_e4m3_bs", out, q, k_cache8, v_cache8, k_scales, v_scales,
-          block_tables, context_lens, workspace, status)
+    _here("pa_decode_window_e4m3_bs", status, out, q, k_cache8, v_cache8, k_scales, v_scales,
+          block_tables, context_lens, workspace)
     rc = load().pa_decode_window_e4m3_bs(
         _ptr(out), _ptr(q), _ptr(k_cache8), _ptr(v_cache8), _ptr(k_scales), _ptr(v_scales),
         _ptr(block_tables), _ptr(context_lens), B, QL, Hq, Hkv, D, bs, block_tables.shape[1], N,
@@ -600,8 +606,8 @@ def pa_prefill_window(out, q, k_cache, v_cache, block_tables, context_lens, q_st
     if out.shape != q.shape or D2 != D or v_cache.shape != k_cache.shape or \
             block_tables.shape[0] != B or q_starts.shape[0] != B + 1:
         raise PagedKVError("pa_prefill_window: inconsistent shapes")
-    _here("pa_prefill_window", out, q, k_cache, v_cache, block_tables, context_lens, q_starts,
-          workspace, status)
+    _here("pa_prefill_window", status, out, q, k_cache, v_cache, block_tables, context_lens,
+          q_starts, workspace)
     rc = load().pa_prefill_window(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
         _ptr(q_starts), T, B, Hq, Hkv, D, bs, block_tables.shape[1], N,
@@ -712,8 +718,8 @@ def _compact_args(what, k_caches, v_caches, src_tables, dst_tables, context_lens
     if dst_tables.shape[0] != B or context_lens.shape[0] != B or keep_lens.shape[0] != B or \
             KB != B or KL not in (1, L) or KH not in (1, Hkv):
         raise PagedKVError("%s: inconsistent shapes" % what)
-    _here(what, *k_caches, *v_caches, src_tables, dst_tables, context_lens, keep, keep_lens,
-          status)
+    _here(what, status, *k_caches, *v_caches, src_tables, dst_tables, context_lens, keep,
+          keep_lens)
     args = [_ptr(src_tables), src_tables.shape[1], _ptr(dst_tables), dst_tables.shape[1],
             _ptr(context_lens), _ptr(keep), _ptr(keep_lens), kmax, int(KL > 1), int(KH > 1), B,
             Hkv, D]
@@ -749,7 +755,7 @@ def pa_compact_tokens_e4m3_bs(k_caches, v_caches, k_scales, v_scales, src_tables
         _need(t, "scales", dtype=torch.float32, ndim=2)
         if t.shape != k_caches[0].shape[:2]:
             raise PagedKVError("pa_compact_tokens_e4m3_bs: inconsistent shapes")
-    _here("pa_compact_tokens_e4m3_bs", *k_scales, *v_scales)
+    _here("pa_compact_tokens_e4m3_bs", None, *k_scales, *v_scales)
     ks = (ctypes.c_void_p * L)(*[t.data_ptr() for t in k_scales])
     vs = (ctypes.c_void_p * L)(*[t.data_ptr() for t in v_scales])
     rc = load().pa_compact_tokens_e4m3_bs(kp, vp, ks, vs, L, *args, bs, N, _ptr(status),
