@@ -460,7 +460,8 @@ pa_status pa_copy_blocks(void* const* k_caches, void* const* v_caches, int num_l
  *   cache[dst_tables[s][i / bs]][h][i % bs][:] = cache[src_tables[s][t / bs]][h][t % bs][:]
  * (the right side as it was before the call), byte for byte.
  *
- *   k_caches, v_caches  HOST arrays of num_layers device pointers (one pool per layer)
+ *   k_caches, v_caches  HOST arrays of num_layers device pointers (one pool per layer, each
+ *                  named once: PA_ERR_INVALID otherwise, as for the scale arrays)
  *   src_tables     device int32 [num_seqs][src_blocks_per_seq], the tables before
  *   dst_tables     device int32 [num_seqs][dst_blocks_per_seq], the tables after; entry i may
  *                  be the sequence's own source entry i (in place) or a block that no source

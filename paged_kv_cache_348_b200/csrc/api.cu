@@ -881,6 +881,15 @@ pa_status pa_copy_blocks(void* const* k_caches, void* const* v_caches, int num_l
 
 namespace {
 
+// No pointer twice among a[0..n) and b[0..n): each names a pool that lists of its own walk, and
+// two walking one pool would overwrite each other's rows.
+bool distinct(const void* const* a, const void* const* b, int n) {
+  for (int i = 0; i < 2 * n; ++i)
+    for (int j = 0; j < i; ++j)
+      if ((i < n ? a[i] : b[i - n]) == (j < n ? a[j] : b[j - n])) return false;
+  return true;
+}
+
 // Arguments shared by the two compaction calls; elem_bytes 1 or 2.
 pa_status compact_args(pkv::CompactArgs& a, void* const* k_caches, void* const* v_caches,
                        int num_layers, const int32_t* src_tables, int src_blocks_per_seq,
@@ -906,6 +915,7 @@ pa_status compact_args(pkv::CompactArgs& a, void* const* k_caches, void* const* 
   for (int l = 0; l < num_layers; ++l)
     if (!k_caches[l] || !v_caches[l] || !aligned16(k_caches[l]) || !aligned16(v_caches[l]))
       return PA_ERR_INVALID;
+  if (!distinct(k_caches, v_caches, num_layers)) return PA_ERR_INVALID;
   a.src_tables = src_tables;
   a.dst_tables = dst_tables;
   a.context_lens = context_lens;
@@ -985,6 +995,9 @@ pa_status pa_compact_tokens_e4m3_bs(void* const* k_caches, void* const* v_caches
   if (!k_scales || !v_scales) return PA_ERR_INVALID;
   for (int l = 0; l < num_layers; ++l)
     if (!k_scales[l] || !v_scales[l]) return PA_ERR_INVALID;
+  if (!distinct(reinterpret_cast<const void* const*>(k_scales),
+                reinterpret_cast<const void* const*>(v_scales), num_layers))
+    return PA_ERR_INVALID;
   for (int l0 = 0; l0 < num_layers; l0 += pkv::kScaledLayersPerLaunch) {
     const int n = std::min(num_layers - l0, pkv::kScaledLayersPerLaunch);
     pkv::ScaledLayerPtrs P;
