@@ -166,7 +166,8 @@ pa_status pa_decode_multi(void* out, const void* q, const void* k_cache, const v
  * the window can be given back, pa_bm_drop_window), as may the cache slots themselves (NaN
  * included).  The rows that some new token sees must be finite for all of its sequence's.
  * Only the visible rows are read from the caches, so the time goes with the window, not the
- * context.
+ * context.  (A segment is cut over at most 12 CTAs: for a few sequences whose window covers all of
+ * a context past some 32768 tokens pa_decode_multi is the faster call.)
  *
  *   q, out         [num_seqs][q_len][num_q_heads][head_dim]
  *   other arguments, limits, workspace and errors as for pa_decode_multi; PA_ERR_INVALID for

@@ -274,11 +274,13 @@ pa_status decode_impl(void* out, const void* q, const void* k_cache, const void*
   if (cap > 0 && grid > cap) grid = cap;
   if (cx.max_grid > 0 && grid > cx.max_grid) grid = cx.max_grid;
   if (cx.mode == pkv::kWindow) {
-    // What a window leaves of a sequence is short and bounded, so few sequences are not cut
-    // over all CTAs: a CTA gets at least kWindowMinUnits units, a segment at most
-    // kWindowMaxSplit CTAs, since their partials meet in one CTA at the end (one sequence,
-    // 32/8 heads, window 1024: 14.1 us against 32 over all CTAs; window 4096: 21.0 against
-    // 37; 12 to 16 units and 8 to 16 CTAs are within 2 us of each other there)
+    // What a window leaves of a sequence is short, so few sequences are not cut over all CTAs: a
+    // CTA gets at least kWindowMinUnits units, a segment at most kWindowMaxSplit CTAs, since
+    // their partials meet in one CTA at the end (one sequence, 32/8 heads, window 1024: 13.1 us
+    // against 31 over all CTAs; window 4096: 19.5 against 35; 12 to 16 units and 8 to 16 CTAs are
+    // within 2 us of each other there).  The constants do not follow the window: at 32768 tokens
+    // both ways take 54 us with 8 kv heads (53 against 210 with one), at 131072 173 against 111
+    // (171 against 215)
     const long long cap = (long long)max_blocks_per_seq * block_size;
     const long long tokens = std::min(
         cap, (long long)cx.window + q_len + 2 * pkv::kUnit + std::min<long long>(cx.num_sinks, cap));

@@ -52,7 +52,9 @@ constexpr int kPfSub = 128;                       // query rows of a subtile (MM
 __host__ __device__ constexpr int pf_tokens(int group) { return kPfSub / group; }
 constexpr int kPfKeys = 128;                      // positions of a key tile
 constexpr int kPfThreads = 384;
-constexpr int kPfPoly = 2;                        // of 16 pairs of weights, those not on ex2
+// of 16 pairs of weights, those not on ex2 (none against two: 24 ragged chunks 48.7 against 47.2
+// us, two prompts of 4000 tokens 218 against 214.5, one of 8000 759 against 755; more were slower)
+constexpr int kPfPoly = 2;
 constexpr int kPfItems = 2;                       // items a CTA has in flight
 constexpr int kPfAlign = 32;                      // granularity of the virtual positions
 
